@@ -25,6 +25,14 @@ LLVQ_FLAG_INDEX_RANGE = 0x1
 LLVQ_FLAG_WAIT_TIMEOUT = 0x2
 LLVQ_FLAG_NOT_CODED = 0x4
 LLVQ_FLAG_SEARCH_INPUT = 0x8
+LLVQ_FLAG_OFFSETS = 0x10
+LLVQ_DTYPE_FP16 = 0
+LLVQ_DTYPE_BF16 = 1
+LLVQ_ACT_NONE = 0
+LLVQ_ACT_RELU = 1
+LLVQ_ACT_GELU = 2
+LLVQ_ACT_GELU_TANH = 3
+LLVQ_ACT_SILU = 4
 LLVQ_SEARCH_ANGULAR = 0
 LLVQ_SEARCH_EUCLIDEAN = 1
 
@@ -39,6 +47,13 @@ class llvq_class96(C.Structure):
     _fields_ = [("start_lo", C.c_uint64), ("start_hi", C.c_uint32), ("meta", C.c_uint32),
                 ("rcp_lo", C.c_uint64), ("rcp_hi", C.c_uint64), ("cum", C.c_uint32 * 4),
                 ("vals", C.c_uint32 * 4)]
+
+
+class llvq_linear_call(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("dtype", C.c_int32), ("activation", C.c_int32), ("gated", C.c_int32),
+                ("experts", C.c_int32), ("x", C.c_void_p), ("x_stride", C.c_int64), ("bias", C.c_void_p),
+                ("residual", C.c_void_p), ("residual_stride", C.c_int64), ("y", C.c_void_p), ("y_stride", C.c_int64),
+                ("offsets", C.c_void_p)]
 
 
 class LLVQError(RuntimeError):
@@ -77,6 +92,11 @@ def lib() -> C.CDLL:
         L.llvq_spherical_gptq_workspace.restype = C.c_size_t
         L.llvq_spherical_gptq.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
                                           C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        L.llvq_linear_workspace.argtypes = [C.c_void_p, C.POINTER(llvq_weight), C.POINTER(llvq_linear_call)]
+        L.llvq_linear_workspace.restype = C.c_size_t
+        for f in ("llvq_linear", "llvq_linear_grouped"):
+            getattr(L, f).argtypes = [C.c_void_p, C.POINTER(llvq_weight), C.POINTER(llvq_linear_call), C.c_void_p,
+                                      C.c_size_t, C.c_void_p]
         L.llvq_set_wait_polls.argtypes = [C.c_uint32, C.c_uint32]
         L.llvq_set_wait_polls.restype = None
         L.llvq_last_error_message.argtypes = []
@@ -84,7 +104,7 @@ def lib() -> C.CDLL:
         L.llvq_class_table96.argtypes = [C.c_int32, C.c_void_p, C.c_int64, C.POINTER(C.c_int64)]
         for f in ("llvq_codec_create", "llvq_codec_info", "llvq_decode", "llvq_gemv",
                   "llvq_gemm_smallbatch", "llvq_get_error", "llvq_decode_noalloc", "llvq_class_table96",
-                  "llvq_encode", "llvq_search", "llvq_spherical_gptq"):
+                  "llvq_encode", "llvq_search", "llvq_spherical_gptq", "llvq_linear", "llvq_linear_grouped"):
             getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
@@ -93,7 +113,8 @@ def lib() -> C.CDLL:
 EXPORTED = ("llvq_codec_create", "llvq_codec_destroy", "llvq_codec_info", "llvq_decode",
             "llvq_gemv", "llvq_gemm_smallbatch", "llvq_get_error", "llvq_status_string",
             "llvq_decode_noalloc", "llvq_class_table96", "llvq_last_error_message", "llvq_encode",
-            "llvq_set_wait_polls", "llvq_search", "llvq_spherical_gptq", "llvq_spherical_gptq_workspace")
+            "llvq_set_wait_polls", "llvq_search", "llvq_spherical_gptq", "llvq_spherical_gptq_workspace",
+            "llvq_linear", "llvq_linear_grouped", "llvq_linear_workspace")
 
 
 def llvq_set_wait_polls(table_polls: int = 0xFFFFFFFF, mma_polls: int = 0xFFFFFFFF) -> None:
@@ -155,6 +176,8 @@ class Codec:
         self.n_points = (hi.value << 64) | lo.value
         self.n_classes = nc.value
         self.word_bytes = 8 if index_bits == 48 else 16
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     @property
     def handle(self) -> C.c_void_p:
@@ -232,6 +255,66 @@ class Codec:
     def gemm(self, w: llvq_weight, X, Y, batch: int, stream=None):
         _check(lib().llvq_gemm_smallbatch(self._h, C.byref(w), C.c_void_p(X.data_ptr()), batch,
                                           C.c_void_p(Y.data_ptr()), _stream(stream)), "llvq_gemm_smallbatch")
+
+    def linear(self, w: llvq_weight, x, y, bias=None, activation: int = LLVQ_ACT_NONE, gated: bool = False,
+               residual=None, workspace=None, stream=None):
+        """A linear layer over the weight w: y = act(x W^T + bias) + residual, or with gated (w's rows are
+        the gate's, then the up projection's) y = act(gate) * up + residual.  x: device fp16 or bf16
+        [tokens, cols]; y and residual: the same type [tokens, outputs]; bias: [w.rows].  Rows may be
+        strided, values within a row not.  residual may be y, and may have one row (or stride 0) for
+        all tokens.  workspace: a device uint8 tensor of at least llvq_linear_workspace bytes, allocated
+        here when None or too small; the one used is returned, to be passed to later calls of the same
+        stream."""
+        return self._linear(lib().llvq_linear, "llvq_linear", w, 0, x, None, y, bias, activation, gated, residual,
+                            workspace, stream)
+
+    def linear_grouped(self, w: llvq_weight, experts: int, x, offsets, y, bias=None, activation: int = LLVQ_ACT_NONE,
+                       gated: bool = False, residual=None, workspace=None, stream=None):
+        """The same with one weight per expert: w holds experts stacked matrices, and expert e takes the rows
+        offsets[e] .. offsets[e + 1] - 1 of x (offsets: device int32 [experts + 1]; it is not read on the
+        host).  bias: [w.rows].  Rows of y that no expert has are left as they were."""
+        return self._linear(lib().llvq_linear_grouped, "llvq_linear_grouped", w, experts, x, offsets, y, bias, activation,
+                            gated, residual, workspace, stream)
+
+    def _linear(self, call, name, w, experts, x, offsets, y, bias, activation, gated, residual, workspace, stream):
+        import torch
+        dtype, rows = x.dtype, w.rows // max(experts, 1)
+        outs = rows // 2 if gated else rows
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"{name}: x is {dtype}, not float16 or bfloat16")
+        tokens = x.shape[0] if x.dim() == 2 else -1
+        if x.shape[-1] != w.cols or tokens < 0:
+            raise ValueError(f"{name}: x is {tuple(x.shape)}, not [tokens, {w.cols}]")
+        for what, t, kind, shape in (("x", x, dtype, None), ("y", y, dtype, (tokens, outs)), ("bias", bias, dtype, None),
+                                     ("residual", residual, dtype, None), ("offsets", offsets, torch.int32, (experts + 1,))):
+            if t is None:
+                continue
+            if t.dtype != kind or t.device != self.device:
+                raise TypeError(f"{name}: {what} is {t.dtype} on {t.device}, not {kind} on {self.device}")
+            if shape is not None and t.shape != shape:
+                raise ValueError(f"{name}: {what} is {tuple(t.shape)}, not {shape}")
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{name}: {what} has a stride of {t.stride(-1)} within its rows")
+        if bias is not None and (bias.numel() != w.rows or not bias.is_contiguous()):
+            raise ValueError(f"{name}: bias is {tuple(bias.shape)}, not {w.rows} contiguous values")
+        res_stride = 0
+        if residual is not None:
+            if residual.shape not in ((tokens, outs), (1, outs), (outs,)):
+                raise ValueError(f"{name}: residual is {tuple(residual.shape)}, not {(tokens, outs)}")
+            res_stride = residual.stride(0) if residual.dim() == 2 and residual.shape[0] == tokens else 0
+        q = llvq_linear_call(tokens, LLVQ_DTYPE_FP16 if dtype is torch.float16 else LLVQ_DTYPE_BF16, activation,
+                             1 if gated else 0, experts, x.data_ptr(), x.stride(0),
+                             None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+                             res_stride, y.data_ptr(), y.stride(0), None if offsets is None else offsets.data_ptr())
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        need = lib().llvq_linear_workspace(self._h, C.byref(w), C.byref(q))
+        if workspace is None or workspace.numel() < need:
+            with torch.cuda.stream(stream):            # the allocator then knows whose memory it is
+                workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=self.device)
+        _check(call(self._h, C.byref(w), C.byref(q), C.c_void_p(workspace.data_ptr()), workspace.numel(),
+                    C.c_void_p(stream.cuda_stream)), name)
+        return workspace
 
     def get_error(self, stream=None) -> int:
         flags = C.c_uint32()

@@ -1,0 +1,289 @@
+// linear.cu -- host side of the compressed linear layers (llvq_linear, llvq_linear_grouped): argument
+// checks, the workspace's layout, tensor maps and the two launches of a call.  Kernels:
+// linear_dequant.cuh, linear_product.cuh.
+#include <algorithm>
+#include <cuda.h>
+
+#include "codec.h"
+#include "linear_dequant.cuh"
+#include "linear_product.cuh"
+
+using namespace llvq;
+
+namespace {
+
+constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
+constexpr long long kMaxRunRows = 0xFFFF;                  // row field of a record
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+uint32_t reciprocal(uint32_t d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u; }
+
+// Makes the codec's device current for a scope.
+struct DeviceScope {
+    int before = -1;
+    bool ok = false, moved = false;
+    explicit DeviceScope(int device) {
+        if (cudaGetDevice(&before) != cudaSuccess) return;
+        ok = before == device || (moved = true, cudaSetDevice(device) == cudaSuccess);
+    }
+    ~DeviceScope() {
+        if (moved) cudaSetDevice(before);
+    }
+};
+
+// The layer of one call and the places of its workspace.
+struct Plan {
+    int experts = 1, rows = 0, outs = 0;                   // matrices, their rows, outputs per token
+    int stage = 0;                                         // LinArgs::stage
+    long long held = 0;                                    // rows of the decoded weight
+    long long xs_pitch = 0;
+    size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
+};
+
+llvq_status refuse(const char *why, llvq_status st = LLVQ_ERR_ARG) {
+    g_last_error = why;
+    return st;
+}
+
+// Checks a call (everything but the workspace) and lays out its workspace.
+llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_linear_call *q, bool grouped, Plan &p) {
+    g_last_error.clear();
+    if (!c || !q) return refuse("null codec or call");
+    const llvq_status st = check_weight(c, w);
+    if (st != LLVQ_OK) return refuse("weight: null or misaligned pointer, size, pitch or budget mismatch");
+    if (w->cols < 1) return refuse("a linear layer has at least one column");
+    if (q->tokens < 0 || q->tokens > 0x7FFFF000ll) return refuse("tokens out of range");
+    if (q->dtype != LLVQ_DTYPE_FP16 && q->dtype != LLVQ_DTYPE_BF16) return refuse("dtype is neither fp16 nor bf16");
+    if (q->activation < LLVQ_ACT_NONE || q->activation > LLVQ_ACT_SILU) return refuse("unknown activation");
+    if (q->gated != 0 && q->gated != 1) return refuse("gated is 0 or 1");
+    if (grouped) {
+        if (q->experts < 1) return refuse("experts out of range");
+        if (q->experts > kLinExperts) return refuse("more than 2048 experts", LLVQ_ERR_UNSUPPORTED);
+        if (w->rows % q->experts) return refuse("the weight's rows are not a multiple of the experts");
+        p.experts = q->experts;
+    } else if (q->experts != 0 && q->experts != 1) {
+        return refuse("experts without groups");
+    }
+    p.rows = w->rows / p.experts;
+    if (q->gated && p.rows % 2) return refuse("a gated layer has an even number of weight rows");
+    p.outs = q->gated ? p.rows / 2 : p.rows;
+    if (q->x_stride < w->cols && q->tokens > 1) return refuse("x_stride below the columns");
+    if (q->y_stride < p.outs && q->tokens > 1) return refuse("y_stride below the outputs");
+    if (q->residual && q->residual_stride < p.outs && q->residual_stride != 0 && q->tokens > 1)
+        return refuse("residual_stride below the outputs and not zero");
+    if (!aligned(q->x, 2) || !aligned(q->y, 2) || !aligned(q->bias, 2) || !aligned(q->residual, 2) || !aligned(q->offsets, 4))
+        return refuse("misaligned pointer");
+    if (w->blocks_per_row > kMaxColumnBlocks) return refuse("more than 65535 blocks per row", LLVQ_ERR_UNSUPPORTED);
+    // only experts that have a token are decoded, and there are at most as many as tokens
+    p.held = (long long)p.rows * std::min<long long>(p.experts, std::max<long long>(q->tokens, 1));
+    if ((p.held + c->num_sms - 1) / c->num_sms + 2 > kMaxRunRows) return refuse("too many rows", LLVQ_ERR_UNSUPPORTED);
+    const bool direct = aligned(q->x, 16) && (q->tokens <= 1 || q->x_stride % 8 == 0);
+    p.stage = q->dtype == LLVQ_DTYPE_BF16 ? 2 : direct ? 0 : 1;
+    p.xs_pitch = ((long long)w->cols + 7) / 8 * 8;
+    size_t at = 0;
+    auto place = [&](size_t bytes) {
+        const size_t here = at;
+        at += round256(bytes);
+        return here;
+    };
+    p.w = place((size_t)p.held * w->blocks_per_row * 48);
+    p.row_scale = place((size_t)p.held * sizeof(float));
+    p.counters = place((size_t)c->pairs * 2 * sizeof(unsigned));
+    p.partial = place((size_t)c->pairs * 2 * kLinTokens * 128 * sizeof(float));
+    if (p.stage) p.xs = place((size_t)q->tokens * p.xs_pitch * sizeof(__half));
+    if (p.stage == 2) p.token_scale = place((size_t)q->tokens * sizeof(float));
+    p.bytes = at;
+    return LLVQ_OK;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+            got != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (EncodeTiled)p;
+    }();
+    return fn;
+}
+
+// fp16 matrix [rows][cols] of the given pitch as a map of boxes of box_rows rows x 64 columns, in the
+// product's swizzled layout; reads beyond rows or cols give zero.
+bool make_map(CUtensorMap &m, const void *base, long long rows, long long cols, long long pitch, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kLpK, (cuuint32_t)box_rows}, unit[2] = {1, 1};
+    return encode_tiled()(&m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(base), dims, strides, box, unit,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch whose prologue may overlap the end of the kernel before it on the stream.
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t st, A &&...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <bool GROUPED>
+cudaError_t launch_dequant(const llvq_codec *c, const llvq_weight *w, const LinArgs &a, cudaStream_t st) {
+    if (c->index_bits == 48) {
+        Dq48Args d{};
+        d.image = (const SmemGv48 *)c->d_gv48;
+        d.npoints = (unsigned long long)c->npoints;
+        d.tabC = c->d_tabC48;
+        d.words = (const unsigned long long *)w->words;
+        d.wait_tries = g_first_wait_tries.load();
+        auto kernel = w->gain_mode == LLVQ_GAIN_FP16_DIRECT ? k_dequant48<0, GROUPED> : k_dequant48<1, GROUPED>;
+        return launch(kernel, c->num_sms, kDqThreads, dq48_smem(GROUPED), st, a, d);
+    }
+    const unsigned long long lo = (unsigned long long)c->npoints, hi = (unsigned long long)(c->npoints >> 64);
+    if (c->index_bits == 72) {
+        const Dec72::Args d{(const Smem72 *)c->d_image, c->d_recs72, c->d_guide72, lo, hi};
+        return launch(k_dequant<Dec72, GROUPED>, c->num_sms * Dec72::kCtasPerSm, 512, dq_smem<Dec72>(GROUPED), st, a, d,
+                      (const Dec72::Word *)w->words);
+    }
+    const Dec96::Args d{(const Smem96 *)c->d_image, c->d_recs96, c->d_guide96, lo, (uint32_t)hi};
+    return launch(k_dequant<Dec96, GROUPED>, c->num_sms * Dec96::kCtasPerSm, 512, dq_smem<Dec96>(GROUPED), st, a, d,
+                  (const Dec96::Word *)w->words);
+}
+
+template <bool GROUPED, bool GATED, class T>
+cudaError_t launch_product(const llvq_codec *c, const LpMaps &m, const LpArgs &a, cudaStream_t st) {
+    return launch(k_linear_product<GROUPED, GATED, T>, 2 * c->pairs, kLpThreads, lp_smem(GROUPED), st, m, a);
+}
+template <bool GROUPED>
+cudaError_t product_dispatch(const llvq_codec *c, const LpMaps &m, const LpArgs &a, bool gated, bool bf16, cudaStream_t st) {
+    if (gated) return bf16 ? launch_product<GROUPED, true, __nv_bfloat16>(c, m, a, st) : launch_product<GROUPED, true, __half>(c, m, a, st);
+    return bf16 ? launch_product<GROUPED, false, __nv_bfloat16>(c, m, a, st) : launch_product<GROUPED, false, __half>(c, m, a, st);
+}
+
+llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_linear_call *q, bool grouped, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    Plan p;
+    const llvq_status st = make_plan(c, w, q, grouped, p);
+    if (st != LLVQ_OK) return st;
+    if (q->tokens == 0 || p.rows == 0) return LLVQ_OK;
+    if (!q->x || !q->y) return refuse("null x or y");
+    if (grouped != (q->offsets != nullptr)) return refuse(grouped ? "null offsets" : "offsets without groups");
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes) return refuse("workspace null, misaligned or too small");
+    DeviceScope scope(c->device);
+    if (!scope.ok) return LLVQ_ERR_CUDA;
+    if (!encode_tiled()) return refuse("the driver has no cuTensorMapEncodeTiled", LLVQ_ERR_CUDA);
+    unsigned char *ws = (unsigned char *)workspace;
+    LpArgs a{};
+    LinArgs &l = a.lin;
+    l.rows = p.rows;
+    l.half = q->gated ? p.rows / 2 : 0;
+    l.cols = w->cols;
+    l.nb = w->blocks_per_row;
+    l.experts = p.experts;
+    l.gain_mode = w->gain_mode;
+    l.gains = (const __half *)w->gains;
+    l.word_pitch = w->row_pitch_words;
+    l.offsets = grouped ? q->offsets : nullptr;
+    l.tokens = q->tokens;
+    l.W = (__half *)(ws + p.w);
+    l.row_scale = (float *)(ws + p.row_scale);
+    l.rows_recip = reciprocal((uint32_t)p.rows);
+    l.nb_recip = reciprocal((uint32_t)l.nb);
+    l.counters = (unsigned *)(ws + p.counters);
+    l.ncounters = 2 * c->pairs;
+    l.stage = p.stage;
+    l.X = q->x;
+    l.ldx = q->x_stride;
+    l.Xs = (__half *)(ws + p.xs);
+    l.ldxs = p.xs_pitch;
+    l.token_scale = (float *)(ws + p.token_scale);
+    l.flags = c->d_flags;
+    a.bias = q->bias;
+    a.residual = q->residual;
+    a.ld_res = q->residual_stride;
+    a.Y = q->y;
+    a.ldy = q->y_stride;
+    a.act = q->activation;
+    a.partial = (float *)(ws + p.partial);
+    a.wait_tries = g_mma_wait_tries.load();
+    LpMaps m;
+    bool ok = make_map(m.w, l.W, p.held, l.cols, (long long)l.nb * 24, 128);
+    const void *x = p.stage ? (const void *)l.Xs : q->x;
+    // the pitch of a single row is never used, but has to be one that a map takes
+    const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;
+    for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.cols, pitch, 128 >> b);
+    if (!ok) return refuse("sizes or strides beyond a tensor map", LLVQ_ERR_UNSUPPORTED);
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool bf16 = q->dtype == LLVQ_DTYPE_BF16;
+    cudaError_t e = grouped ? launch_dequant<true>(c, w, l, s) : launch_dequant<false>(c, w, l, s);
+    if (e == cudaSuccess)
+        e = grouped ? product_dispatch<true>(c, m, a, q->gated, bf16, s) : product_dispatch<false>(c, m, a, q->gated, bf16, s);
+    if (e == cudaSuccess) return LLVQ_OK;
+    return refuse(cudaGetErrorString(e), LLVQ_ERR_CUDA);
+}
+
+template <class K>
+void allow(K kernel, size_t smem) {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+template <bool GROUPED>
+void allow_all() {
+    allow(k_dequant48<0, GROUPED>, dq48_smem(GROUPED));
+    allow(k_dequant48<1, GROUPED>, dq48_smem(GROUPED));
+    allow(k_dequant<Dec72, GROUPED>, dq_smem<Dec72>(GROUPED));
+    allow(k_dequant<Dec96, GROUPED>, dq_smem<Dec96>(GROUPED));
+    allow(k_linear_product<GROUPED, false, __half>, lp_smem(GROUPED));
+    allow(k_linear_product<GROUPED, true, __half>, lp_smem(GROUPED));
+    allow(k_linear_product<GROUPED, false, __nv_bfloat16>, lp_smem(GROUPED));
+    allow(k_linear_product<GROUPED, true, __nv_bfloat16>, lp_smem(GROUPED));
+}
+
+}  // namespace
+
+void llvq::set_linear_attrs(llvq_codec *c) {
+    static_assert(dq48_smem(true) <= 232448 && lp_smem(true) <= 232448, "shared memory of an SM");
+    allow_all<false>();
+    allow_all<true>();
+    // pairs of CTAs that are resident at once, one CTA per SM
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(c->num_sms / 2 * 2));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = lp_smem(true);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear_product<true, false, __half>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = c->num_sms / 2;
+    }
+    c->pairs = std::max(1, std::min(n, c->num_sms / 2));
+}
+
+extern "C" {
+
+size_t llvq_linear_workspace(const llvq_codec *c, const llvq_weight *w, const llvq_linear_call *q) {
+    Plan p;
+    return make_plan(c, w, q, q && q->experts > 0, p) == LLVQ_OK ? p.bytes : 0;
+}
+
+llvq_status llvq_linear(const llvq_codec *c, const llvq_weight *w, const llvq_linear_call *q, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    return run_linear(c, w, q, false, workspace, workspace_bytes, stream);
+}
+
+llvq_status llvq_linear_grouped(const llvq_codec *c, const llvq_weight *w, const llvq_linear_call *q, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    return run_linear(c, w, q, true, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,228 @@
+// linear_common.cuh -- what the kernels of the compressed linear layers share: the arguments of a
+// call, the groups of tokens, the row and token scales, and the epilogue's activations.
+//
+// A linear layer over a compressed weight (papernotes.org notes, 方法详解 / 关键设计 4 gives the
+// product; bias, activation, residual, gating and experts are what a language model puts around it):
+//
+//   z[t][r] = sum_k w[r][k] x[t][k] + b[r]        y[t][o] = act(z[t][o]) [* z[t][F + o]] + res[t][o]
+//
+// runs as two kernels: the blocks are decoded once into an fp16 weight in the caller's workspace
+// (linear_dequant.cuh), and a tile product on the tensor cores multiplies it with every token and
+// applies the epilogue (linear_product.cuh).
+//
+// Scales.  A weight is stored as fp16(w 2^s) with one power of two per row, chosen so that the
+// row's largest gain lies just below the end of the fp16 range: no row, however small or large,
+// meets fp16's subnormals or overflows, and w keeps 11 significant bits.  bf16 activations are
+// restated as fp16(x 2^u) with one power of two per token: 8 significant bits fit in 11, so the
+// restatement is exact down to 2^-28 of the token's largest value and off by at most 2^-39 of it
+// below that, less than the fp32 accumulation of the product rounds.  Both powers leave again in
+// the epilogue, exactly.  A bf16 weight would have lost 3 bits that fp16 keeps.
+#pragma once
+#include <cuda_bf16.h>
+#include "codec48.cuh"
+
+namespace llvq {
+
+constexpr int kLinExperts = 2048;             // most experts of one call (their groups sit in shared memory)
+constexpr int kLinRows = 256;                 // weight rows of a tile (one pair of CTAs)
+constexpr int kLinTokens = 256;               // most tokens of a tile
+
+struct LinArgs {
+    // the layer: `experts` stacked matrices of `rows` rows; half = rows / 2 when gated, else 0
+    int rows, half, cols, nb, experts;
+    int gain_mode;
+    const __half *gains;
+    long long word_pitch;
+    // tokens: offsets (experts + 1 entries) or null for one matrix and every token
+    const int *offsets;
+    long long tokens;
+    // the decoded weight [active expert][row] (gated: row pairs gate, up interleaved), pitch nb * 24,
+    // and 1 / (its power of two) per row
+    __half *W;
+    float *row_scale;
+    uint32_t rows_recip, nb_recip;            // ceil(2^32 / rows), ceil(2^32 / nb) (0 for 1)
+    // the split tiles' arrival counters
+    unsigned *counters;
+    int ncounters;
+    // activations restated in the workspace: stage 0 none, 1 fp16 copied, 2 bf16 to fp16 with scales
+    int stage;
+    const void *X;
+    long long ldx;
+    __half *Xs;
+    long long ldxs;
+    float *token_scale;
+    unsigned *flags;
+};
+
+// n / d for n < 2^32 by a multiply-high with recip = ceil(2^32 / d): the product overshoots by less
+// than n / 2^32 < 1, so one correction makes it exact.
+__device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t d, uint32_t recip) {
+    if (recip == 0u) return n;                                  // d = 1
+    uint32_t q = __umulhi(n, recip);
+    if ((unsigned long long)q * d > n) q--;
+    return q;
+}
+
+// row of the decoded weight that holds row r of a matrix
+__device__ __forceinline__ int lin_place(int r, int half) {
+    return half == 0 ? r : r < half ? 2 * r : 2 * (r - half) + 1;
+}
+
+// The experts that have tokens, in order, by one warp: id[i], and with EDGES their token ranges
+// lo[i], hi[i].  Offsets that fall, start below zero or end beyond the tokens leave no expert (the
+// flag is raised by the caller); returns the count, or -1 for such offsets.
+template <bool EDGES>
+__device__ __forceinline__ int lin_groups(const LinArgs &a, int *id, int *lo, int *hi) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        int s = 0, t = 0;
+        if (e < a.experts) {
+            s = __ldg(a.offsets + e);
+            t = __ldg(a.offsets + e + 1);
+            bad |= t < s || s < 0 || (long long)t > a.tokens;
+        }
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, t > s);
+        if (t > s) {
+            const int i = n + __popc(m & ((1u << lane) - 1u));
+            id[i] = e;
+            if (EDGES) {
+                lo[i] = s;
+                hi[i] = t;
+            }
+        }
+        n += __popc(m);
+    }
+    return __any_sync(0xFFFFFFFFu, bad) ? -1 : n;
+}
+
+// largest finite magnitude, as its fp32 bits (ordered like the values)
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) {
+    return __reduce_max_sync(0xFFFFFFFFu, v);
+}
+// 2^k for -126 <= k <= 127, and its inverse from its bits
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(0x7F000000u - __float_as_uint(p)); }
+
+// The scale of one row of gains, by one warp: 2^-s with s such that the row's largest weight lies in
+// the top binades of fp16.  Table gains bound the weights themselves (a direction's coordinates are
+// at most 1), direct gains leave out |v_i| < 64.
+__device__ __forceinline__ float lin_row_scale(const LinArgs &a, long long row) {
+    const int lane = threadIdx.x & 31;
+    uint32_t top = 0;
+    if (a.gain_mode == 0) {
+        const __half *g = a.gains + row * a.nb;
+        for (int j = lane; j < a.nb; j += 32) top = max(top, finite_bits(__half2float(__ldg(g + j))));
+    } else {
+        const __half *g = a.gains + row * 256;
+        if (((unsigned long long)a.gains & 15ull) == 0ull) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(g) + lane);
+            const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
+            }
+        } else {
+            for (int j = lane; j < 256; j += 32) top = max(top, finite_bits(__half2float(__ldg(g + j))));
+        }
+    }
+    top = warp_max(top);
+    if (top == 0u) return 1.f;
+    const int ex = (int)(top >> 23) - 127;                      // fp16 values: -24 .. 15
+    return pow2(ex - (a.gain_mode == 0 ? 9 : 14));
+}
+
+// Eight consecutive 16-bit values from element i of a row; elements at and beyond n read as zero.
+__device__ __forceinline__ uint4 lin_load8(const uint16_t *row, int i, int n, bool wide) {
+    if (wide && i + 8 <= n) return __ldg(reinterpret_cast<const uint4 *>(row + i));
+    uint32_t h[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+        if (i + k < n) h[k >> 1] |= (uint32_t)__ldg(row + i + k) << (16 * (k & 1));
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// One token restated for the product, by one warp: fp16 copied to an aligned row (no scale), bf16 scaled by a
+// power of two and rounded to fp16 (see above).  The row is read twice; the second time it is in L1.
+__device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, int cols, float *scale) {
+    const int lane = threadIdx.x & 31;
+    const bool wide = (((unsigned long long)src) & 15ull) == 0ull;
+    const int n8 = (cols + 7) / 8;
+    if (!scale) {
+#pragma unroll 4
+        for (int i = lane; i < n8; i += 32) dst[i] = lin_load8(src, 8 * i, cols, wide);
+        return;
+    }
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int i = lane; i < n8; i += 32) {
+        const uint4 q = lin_load8(src, 8 * i, cols, wide);
+        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            top = max(top, max(finite_bits(__uint_as_float(h[k] << 16)), finite_bits(__uint_as_float(h[k] & 0xFFFF0000u))));
+    }
+    top = warp_max(top);
+    // the largest value's exponent (subnormals: -126 stands for all of them); 2^126 is the most a
+    // scale's inverse can be
+    const int ex = max((int)(top >> 23) - 127, -126);
+    const float inv = pow2(top == 0u ? 0 : max(ex - 14, -126)), f = pow2_inverse(inv);
+    if (lane == 0) *scale = inv;
+#pragma unroll 4
+    for (int i = lane; i < n8; i += 32) {
+        const uint4 q = lin_load8(src, 8 * i, cols, wide);
+        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const __half2 v = __floats2half2_rn(__uint_as_float(h[k] << 16) * f, __uint_as_float(h[k] & 0xFFFF0000u) * f);
+            o[k] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// Activations on a few values of one thread (the branch is uniform over the grid).  Each is written
+// so that its negative tail keeps its relative accuracy: x / (1 + e^-u) instead of a sum with 1.
+enum LinAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+template <int N>
+__device__ __forceinline__ void lin_activate(float (&z)[N], int act) {
+    switch (act) {
+        case kActRelu:
+#pragma unroll
+            for (int i = 0; i < N; i++) z[i] = z[i] < 0.f ? 0.f : z[i];        // NaN stays
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int i = 0; i < N; i++) z[i] = 0.5f * z[i] * erfcf(-0.70710678118654752f * z[i]);
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float u = 1.5957691216057308f * (z[i] + 0.044715f * z[i] * z[i] * z[i]);   // 2 sqrt(2 / pi)
+                z[i] = z[i] / (1.f + __expf(-u));
+            }
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int i = 0; i < N; i++) z[i] = z[i] / (1.f + __expf(-z[i]));
+            break;
+        default: break;
+    }
+}
+
+template <class T> __device__ __forceinline__ float lin_load(const T *p);
+template <> __device__ __forceinline__ float lin_load<__half>(const __half *p) { return __half2float(*p); }
+template <> __device__ __forceinline__ float lin_load<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+template <class T> __device__ __forceinline__ T lin_round(float v);
+template <> __device__ __forceinline__ __half lin_round<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 lin_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+}  // namespace llvq

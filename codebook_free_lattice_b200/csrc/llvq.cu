@@ -28,6 +28,7 @@
 #include "encode96.cuh"
 #include "search48.cuh"
 #include "gptq48.cuh"
+#include "codec.h"
 #include "tables.h"
 #include "tables96.h"
 
@@ -37,37 +38,15 @@ static_assert(kFlagIndexRange == LLVQ_FLAG_INDEX_RANGE && kFlagWaitTimeout == LL
                   kFlagNotCoded == LLVQ_FLAG_NOT_CODED && kFlagSearchInput == LLVQ_FLAG_SEARCH_INPUT,
               "device flag bits match the C ABI");
 
-struct llvq_codec {
-    int index_bits = 0;
-    int device = -1;
-    int M = 0;
-    u128 npoints = 0;
-    int64_t nclasses = 0;
-    int num_sms = 0;
-    void *d_image = nullptr;       // Smem48 / Smem72 image (copied to shared memory per CTA)
-    Rec72 *d_recs72 = nullptr;     // 72-bit class records (global memory)
-    uint32_t *d_guide72 = nullptr; // 72-bit guide table
-    Rec96 *d_recs96 = nullptr;     // 96-bit class records (global memory)
-    uint32_t *d_guide96 = nullptr; // 96-bit guide table (top 28 index bits)
-    void *d_even48 = nullptr;      // SmemEven48 image (48-bit table path)
-    uint32_t *d_tabC48 = nullptr;  // complement arrangement tables (48-bit table path)
-    void *d_gv48 = nullptr;        // SmemGv48 image (48-bit fused products, k_gemv48)
-    void *d_enc48 = nullptr;       // EncSmem48 image (48-bit encoder)
-    void *d_search48 = nullptr;    // SearchImage48 (48-bit nearest-point search)
-    void *d_enc72 = nullptr;       // EncSmem72 image (72-bit encoder)
-    unsigned long long *d_keys72 = nullptr;  // 72-bit class keys (encoder)
-    void *d_enc96 = nullptr;       // EncSmem96 image (96-bit encoder)
-    unsigned long long *d_keys96 = nullptr;  // 96-bit class keys (encoder, built on the device)
-    unsigned *d_flags = nullptr;   // sticky device flags
-};
-
-namespace {
-
+namespace llvq {
 thread_local std::string g_last_error;
 // polls of a kernel's first bounded wait on its table copy and on its tensor-core products
 // (llvq_set_wait_polls; tests set them to 0 to take the timeout paths)
 std::atomic<uint32_t> g_first_wait_tries{kBulkWaitTries};
 std::atomic<uint32_t> g_mma_wait_tries{kMmaWaitTries};
+}  // namespace llvq
+
+namespace {
 
 // 48-bit batches from this size up run on the tensor cores (k_gemm_tc48); smaller ones, and every
 // 72/96-bit batch, on the CUDA cores
@@ -921,7 +900,9 @@ cudaError_t gemm_dispatch(const llvq_codec *c, typename D::Args a, const llvq_we
     }
 }
 
-llvq_status check_weight(const llvq_codec *c, const llvq_weight *w) {
+}  // namespace
+
+llvq_status llvq::check_weight(const llvq_codec *c, const llvq_weight *w) {
     if (!w || !w->words || !w->gains) return LLVQ_ERR_ARG;
     if (w->rows < 0 || w->cols < 0 || w->blocks_per_row < 0) return LLVQ_ERR_ARG;
     if (w->blocks_per_row != (w->cols + 23) / 24) return LLVQ_ERR_ARG;
@@ -932,8 +913,6 @@ llvq_status check_weight(const llvq_codec *c, const llvq_weight *w) {
     if (!aligned(w->words, (size_t)w->word_bytes) || !aligned(w->gains, 2)) return LLVQ_ERR_ARG;
     return LLVQ_OK;
 }
-
-}  // namespace
 
 // ---- decode without any device allocation -----------------------------------------------
 // A caller that cannot allocate device memory (under a framework's memory pool that owns every
@@ -1024,6 +1003,7 @@ llvq_status codec_create96(llvq_codec **out) {
         return st;
     }
     set_kernel_attrs();
+    set_linear_attrs(c);
     *out = c;
     return LLVQ_OK;
 }
@@ -1183,6 +1163,7 @@ llvq_status llvq_codec_create(int32_t index_bits, llvq_codec **out) {
         return LLVQ_ERR_CUDA;
     }
     set_kernel_attrs();
+    set_linear_attrs(c);
     *out = c;
     return LLVQ_OK;
 }

@@ -61,10 +61,23 @@ typedef enum {
                                        the output of that call is incomplete */
 #define LLVQ_FLAG_NOT_CODED 0x4u    /* llvq_encode met a vector that is not a coded lattice point */
 #define LLVQ_FLAG_SEARCH_INPUT 0x8u /* llvq_search met a row holding a NaN or an infinity */
+#define LLVQ_FLAG_OFFSETS 0x10u     /* llvq_linear_grouped met offsets that fall or leave the tokens;
+                                       that call wrote no output */
 
 /* Criteria of llvq_search. */
 #define LLVQ_SEARCH_ANGULAR 0       /* maximize <x, v> / |v| (the shape of a shape-gain split) */
 #define LLVQ_SEARCH_EUCLIDEAN 1     /* minimize |x - scale * v| (spherical clipping) */
+
+/* Types of a linear layer's activations, bias, residual and output. */
+#define LLVQ_DTYPE_FP16 0
+#define LLVQ_DTYPE_BF16 1
+
+/* Activations of a linear layer. */
+#define LLVQ_ACT_NONE 0             /* z */
+#define LLVQ_ACT_RELU 1             /* max(z, 0) */
+#define LLVQ_ACT_GELU 2             /* z / 2 (1 + erf(z / sqrt 2)) */
+#define LLVQ_ACT_GELU_TANH 3        /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+#define LLVQ_ACT_SILU 4             /* z / (1 + exp(-z)) */
 
 /* Opaque codec: owns the decode tables of one index budget on one device. */
 typedef struct llvq_codec llvq_codec;
@@ -237,6 +250,60 @@ llvq_status llvq_search(const llvq_codec *codec, int32_t max_shell, int32_t mode
 size_t llvq_spherical_gptq_workspace(int32_t rows, int32_t cols);
 llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int32_t rows, int32_t cols,
                                 double *d_W, const double *d_U, int8_t *d_points, double *d_norms,
+                                void *d_workspace, size_t workspace_bytes, void *stream);
+
+/* Linear layer over a compressed weight, any number of tokens.  The fused product of 关键设计 4 with what
+ * a language model puts around it (bias, activation, gate, residual, experts), which the paper does
+ * not describe:
+ *   z[t][r] = sum_k w[r][k] x[t][k] + bias[r]
+ *   y[t][o] = act(z[t][o])                        + residual[t][o]     gated = 0, o < F = rows
+ *   y[t][o] = act(z[t][o]) * z[t][F + o]          + residual[t][o]     gated = 1, o < F = rows / 2
+ * (a gated weight holds the gate's rows, then the up projection's).  x, bias, residual and y are of
+ * `dtype`; sums, bias, activation and residual are held in fp32 and y is rounded once.  Each decoded
+ * weight is rounded to 11 significant bits (fp16 with a power of two per row), for bf16 activations
+ * too.  Rows of x and y may have any stride and start at any 2-byte aligned address; rows of y may
+ * be the residual's (same address and stride), but not x's.
+ *
+ * llvq_linear: `experts` 0 or 1, `offsets` NULL: tokens rows of x, one matrix.
+ * llvq_linear_grouped: `experts` (1 .. 2048) matrices of rows / experts rows each, stacked in w; bias
+ * [experts][rows / experts].  Expert e takes the tokens offsets[e] .. offsets[e + 1] - 1 (device int32
+ * [experts + 1], not falling, offsets[0] >= 0, offsets[experts] <= tokens); rows of y outside
+ * offsets[0] .. offsets[experts] - 1 are left as they were and the same rows of x and residual are not
+ * used.  An expert without tokens costs nothing: its blocks are not decoded.  Offsets that fall or leave
+ * 0 .. tokens raise LLVQ_FLAG_OFFSETS, and then nothing of y is written. */
+typedef struct {
+    int64_t tokens;            /* rows of x, residual and y (the room, for grouped calls) */
+    int32_t dtype;             /* LLVQ_DTYPE_* */
+    int32_t activation;        /* LLVQ_ACT_* */
+    int32_t gated;             /* 0 or 1 */
+    int32_t experts;           /* grouped: stacked matrices; else 0 or 1 */
+    const void *x;             /* device [tokens][cols] */
+    int64_t x_stride;          /* elements between rows, >= cols (not used for one token) */
+    const void *bias;          /* device [weight rows], or NULL */
+    const void *residual;      /* device [tokens][F], or NULL */
+    int64_t residual_stride;   /* >= F, or 0 for one row added to every token */
+    void *y;                   /* device [tokens][F], overwritten */
+    int64_t y_stride;          /* >= F */
+    const int32_t *offsets;    /* grouped: device [experts + 1]; else NULL */
+} llvq_linear_call;
+
+/* Bytes of workspace that a call needs (0 when its sizes or types are refused): the decoded weight of the
+ * experts that can have tokens (48 bytes per block), partial sums (19.5 MB on 148 SMs), and for bf16 or
+ * unaligned x the activations restated in fp16.  Depends on x's address only by its 16-byte alignment;
+ * the sizes and x must be set in `call`, its other pointers need not be.  A call with experts >= 1 is
+ * taken as grouped. */
+size_t llvq_linear_workspace(const llvq_codec *codec, const llvq_weight *w, const llvq_linear_call *call);
+
+/* The layer: two launches on `stream` (decode, product with epilogue), no allocation, no synchronisation;
+ * the codec's device is made current for the call.  d_workspace: device, 256-byte aligned, owned by the
+ * caller, contents not kept between calls; calls that may overlap (other streams, graphs replayed at
+ * once) each need their own.  cols >= 1; at most 65535 blocks per row.  48-, 72- and 96-bit codecs, both
+ * gain modes.  Results do not depend on timing: sums are taken in a fixed order.  An index >= N_M
+ * contributes nothing and raises LLVQ_FLAG_INDEX_RANGE.  The reason of a refusal is in
+ * llvq_last_error_message. */
+llvq_status llvq_linear(const llvq_codec *codec, const llvq_weight *w, const llvq_linear_call *call, void *d_workspace,
+                        size_t workspace_bytes, void *stream);
+llvq_status llvq_linear_grouped(const llvq_codec *codec, const llvq_weight *w, const llvq_linear_call *call,
                                 void *d_workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, return the sticky device flags raised since the last call in *flags
