@@ -37,7 +37,7 @@ struct Plan {
     int experts = 1, rows = 0, outs = 0;                   // matrices, their rows, outputs per token
     int stage = 0;                                         // LinArgs::stage
     long long held = 0;                                    // rows of the decoded weight
-    long long xs_pitch = 0;
+    long long w_pitch = 0, xs_pitch = 0;
     size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
 };
 
@@ -80,16 +80,18 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
     if ((p.held + c->num_sms - 1) / c->num_sms + 2 > kMaxRunRows) return refuse("too many rows", LLVQ_ERR_UNSUPPORTED);
     const bool direct = aligned(q->x, 16) && (q->tokens <= 1 || q->x_stride % 8 == 0);
     p.stage = q->dtype == LLVQ_DTYPE_BF16 ? 2 : direct ? 0 : 1;
-    p.xs_pitch = ((long long)w->cols + 7) / 8 * 8;
+    // whole 128-byte lines per row: a box row that straddles two lines costs the tensor copies twice
+    p.w_pitch = ((long long)w->blocks_per_row * 24 + 63) / 64 * 64;
+    p.xs_pitch = ((long long)w->cols + 63) / 64 * 64;
     size_t at = 0;
     auto place = [&](size_t bytes) {
         const size_t here = at;
         at += round256(bytes);
         return here;
     };
-    p.w = place((size_t)p.held * w->blocks_per_row * 48);
+    p.w = place((size_t)p.held * p.w_pitch * sizeof(__half));
     p.row_scale = place((size_t)p.held * sizeof(float));
-    p.counters = place((size_t)c->pairs * 2 * sizeof(unsigned));
+    p.counters = place((size_t)c->pairs * kLpCounters * sizeof(unsigned));
     p.partial = place((size_t)c->pairs * 2 * kLinTokens * 128 * sizeof(float));
     if (p.stage) p.xs = place((size_t)q->tokens * p.xs_pitch * sizeof(__half));
     if (p.stage == 2) p.token_scale = place((size_t)q->tokens * sizeof(float));
@@ -198,11 +200,12 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     l.offsets = grouped ? q->offsets : nullptr;
     l.tokens = q->tokens;
     l.W = (__half *)(ws + p.w);
+    l.ldw = p.w_pitch;
     l.row_scale = (float *)(ws + p.row_scale);
     l.rows_recip = reciprocal((uint32_t)p.rows);
     l.nb_recip = reciprocal((uint32_t)l.nb);
     l.counters = (unsigned *)(ws + p.counters);
-    l.ncounters = 2 * c->pairs;
+    l.ncounters = c->pairs * kLpCounters;
     l.stage = p.stage;
     l.X = q->x;
     l.ldx = q->x_stride;
@@ -219,7 +222,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     a.partial = (float *)(ws + p.partial);
     a.wait_tries = g_mma_wait_tries.load();
     LpMaps m;
-    bool ok = make_map(m.w, l.W, p.held, l.cols, (long long)l.nb * 24, 128);
+    bool ok = make_map(m.w, l.W, p.held, l.cols, l.ldw, 128);
     const void *x = p.stage ? (const void *)l.Xs : q->x;
     // the pitch of a single row is never used, but has to be one that a map takes
     const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;

@@ -36,9 +36,10 @@ struct LinArgs {
     // tokens: offsets (experts + 1 entries) or null for one matrix and every token
     const int *offsets;
     long long tokens;
-    // the decoded weight [active expert][row] (gated: row pairs gate, up interleaved), pitch nb * 24,
+    // the decoded weight [active expert][row] (gated: row pairs gate, up interleaved), rows of ldw values,
     // and 1 / (its power of two) per row
     __half *W;
+    long long ldw;
     float *row_scale;
     uint32_t rows_recip, nb_recip;            // ceil(2^32 / rows), ceil(2^32 / nb) (0 for 1)
     // the split tiles' arrival counters
@@ -189,38 +190,48 @@ __device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, in
     }
 }
 
-// Activations on a few values of one thread (the branch is uniform over the grid).  Each is written
-// so that its negative tail keeps its relative accuracy: x / (1 + e^-u) instead of a sum with 1.
+// Activations, four values at a time and out of line: the code of one activation is fetched once, and
+// a kernel that needs none of it does not step over it.  Each is written so that its negative tail keeps
+// its accuracy: z / (1 + e^-u), and for gelu the complementary error function by the rational
+// approximation 7.1.26 of Abramowitz and Stegun, erfc(x) = t (a1 + t (a2 + ...)) e^-x^2 with t = 1 / (1 + p x),
+// off by at most 1.5e-7 (a fifth of the instructions of erfcf, whose last bits a 16-bit output drops).
+// The quick division and exponential are good to a few fp32 steps; a denominator beyond 2^126 gives 0, the limit.
 enum LinAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+__device__ __forceinline__ float lin_activate1(float z, int act) {
+    if (act == kActRelu) return z < 0.f ? 0.f : z;                              // NaN stays
+    if (act == kActGelu) {
+        const float x = fabsf(z) * 0.70710678118654752f;
+        const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+        float q = fmaf(1.061405429f, t, -1.453152027f);
+        q = fmaf(q, t, 1.421413741f);
+        q = fmaf(q, t, -0.284496736f);
+        q = fmaf(q, t, 0.254829592f);
+        const float tail = 0.5f * q * t * __expf(-x * x);                       // P(|z|): z or less at -|z|
+        return z * (z < 0.f ? tail : 1.f - tail);
+    }
+    const float u = act == kActSilu ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);     // 2 sqrt(2 / pi)
+    return __fdividef(z, 1.f + __expf(-u));
+}
+__device__ __noinline__ float4 lin_activate4(float4 z, int act) {
+    return make_float4(lin_activate1(z.x, act), lin_activate1(z.y, act), lin_activate1(z.z, act), lin_activate1(z.w, act));
+}
 template <int N>
 __device__ __forceinline__ void lin_activate(float (&z)[N], int act) {
-    switch (act) {
-        case kActRelu:
+    if (act == kActNone) return;
 #pragma unroll
-            for (int i = 0; i < N; i++) z[i] = z[i] < 0.f ? 0.f : z[i];        // NaN stays
-            break;
-        case kActGelu:
-#pragma unroll
-            for (int i = 0; i < N; i++) z[i] = 0.5f * z[i] * erfcf(-0.70710678118654752f * z[i]);
-            break;
-        case kActGeluTanh:
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                const float u = 1.5957691216057308f * (z[i] + 0.044715f * z[i] * z[i] * z[i]);   // 2 sqrt(2 / pi)
-                z[i] = z[i] / (1.f + __expf(-u));
-            }
-            break;
-        case kActSilu:
-#pragma unroll
-            for (int i = 0; i < N; i++) z[i] = z[i] / (1.f + __expf(-z[i]));
-            break;
-        default: break;
+    for (int i = 0; i < N; i += 4) {
+        const float4 y = lin_activate4(make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]), act);
+        z[i] = y.x;
+        z[i + 1] = y.y;
+        z[i + 2] = y.z;
+        z[i + 3] = y.w;
     }
 }
 
 template <class T> __device__ __forceinline__ float lin_load(const T *p);
 template <> __device__ __forceinline__ float lin_load<__half>(const __half *p) { return __half2float(*p); }
 template <> __device__ __forceinline__ float lin_load<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+template <class T> __device__ __forceinline__ float lin_float(T v) { return lin_load(&v); }
 template <class T> __device__ __forceinline__ T lin_round(float v);
 template <> __device__ __forceinline__ __half lin_round<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 lin_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }

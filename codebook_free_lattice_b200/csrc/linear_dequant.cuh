@@ -177,7 +177,7 @@ __device__ __forceinline__ void dq48_consume(const LinArgs &a, const SmemGv48 &S
 #pragma unroll
         for (int q = 0; q < 6; q++) i8x4_to_h2x2(v[q], wh[2 * q], wh[2 * q + 1]);
     }
-    dq_store<GAIN>(wh, scale, a.W + (dst * a.nb + j) * 24);
+    dq_store<GAIN>(wh, scale, a.W + dst * a.ldw + j * 24);
 }
 
 template <int GAIN, bool GROUPED>
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
             bad = true;
             long long src, dst;
             dq_row<GROUPED>(a, H.id, run.row0 + (int)rl, src, dst);
-            dq_store_zero(a.W + (dst * nb + (b - rl * (uint32_t)nb)) * 24);
+            dq_store_zero(a.W + dst * a.ldw + (b - rl * (uint32_t)nb) * 24);
         }
         append(prec, pk);
         prec = rec;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typen
 #pragma unroll
         for (int q = 0; q < 6; q++) i8x4_to_h2x2(ok ? v[q] : 0u, wh[2 * q], wh[2 * q + 1]);
         const float f = pow2_inverse(a.row_scale[dst]);
-        __half *out = a.W + (dst * a.nb + j) * 24;
+        __half *out = a.W + dst * a.ldw + j * 24;
         if (!ok) dq_store_zero(out);
         else if (a.gain_mode == 0) dq_store<0>(wh, f * __half2float(__ldg(a.gains + src * a.nb + j)), out);
         else dq_store<1>(wh, f * (__half2float(__ldg(a.gains + src * 256 + D::gain_code(w))) * D::invnorm(S, m)), out);

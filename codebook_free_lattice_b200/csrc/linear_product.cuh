@@ -11,8 +11,9 @@
 // run the epilogue.
 //
 // A persistent grid walks the tiles of all groups.  Tiles that do not fill a last round of pairs are
-// split along K over the idle pairs; partial sums go through the workspace and the pair that arrives
-// last adds them in the order of the splits, so results do not depend on timing.
+// split along K over the idle pairs; partial sums go through the workspace, and whichever pair brings the
+// last part of a chunk of 16 columns adds its parts in the order of the splits, so results do not
+// depend on timing and the adding spreads over the pairs.
 #pragma once
 #include <cuda.h>
 #include "linear_common.cuh"
@@ -28,12 +29,13 @@ constexpr int kLpBBytes = kLinTokens / 2 * kLpK * 2;       // up to 128 tokens
 constexpr int kLpStageBytes = kLpABytes + kLpBBytes;
 constexpr int kLpBand = 8;                                 // row tiles of a band (L2 reuse of the tokens)
 constexpr int kLpMinSplit = 4;                             // least K stages of a split
+constexpr int kLpCounters = 2 * 4 * 16;                    // per split tile: CTA, warp quarter, chunk of 16 columns
 
 struct LpShared {
     unsigned long long full[kLpStages], empty[kLpStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
-    int abort, nact, last;
-    int tiles, whole, split, units;
+    int abort, nact, pad;
+    int whole, split, units, pad2;
     int id[kLinExperts], lo[kLinExperts], hi[kLinExperts], first[kLinExperts + 1];
 };
 __host__ __device__ constexpr size_t lp_smem(bool grouped) {
@@ -51,10 +53,20 @@ struct LpArgs {
     void *Y;
     long long ldy;
     int act;
-    float *partial;                                        // [pairs][2][tokens of a tile][128]
+    float *partial;                                        // [pairs][2][tokens of a tile / 4][128][4]
     uint32_t wait_tries;
 };
 
+// One lane of a converged warp.  The loading and the issuing warp run their loops whole and with values
+// that are uniform over the warp, and elect a lane for the instructions themselves: under a plain
+// `lane == 0` the operands, which these instructions take from uniform registers, cost several times as much to
+// bring there (0.43 us per stage of 64 columns instead of what the products take).
+__device__ __forceinline__ bool lp_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int lp_uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ uint32_t lp_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -107,17 +119,17 @@ __device__ __forceinline__ void lp_commit(uint32_t bar) {             // to this
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  ::"r"(bar), "h"((unsigned short)3) : "memory");
 }
-__device__ __forceinline__ void lp_tmem_load(uint32_t addr, uint32_t (&v)[32]) {
+__device__ __forceinline__ void lp_tmem_load(uint32_t addr, float (&z)[16]) {
+    uint32_t v[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
+#pragma unroll
+    for (int c = 0; c < 16; c++) z[c] = __uint_as_float(v[c]);
 }
 
 // One unit of a pair's work: a tile, or one K split of it.
@@ -129,7 +141,7 @@ struct LpUnit {
     int split, slot, tile;                    // splits of the tile (1: whole), partial slot of this one, counter
 };
 template <bool GROUPED>
-__device__ __forceinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u, int nk) {
+__device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u, int nk) {
     LpUnit x;
     int tile = u, part = 0;
     x.split = 1;
@@ -172,56 +184,89 @@ __device__ __forceinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, in
     return x;
 }
 
-// The outputs of N columns (tokens t ..) of this thread's weight row, from its accumulators.
-template <bool GATED, class T, int N>
-__device__ __forceinline__ void lp_outputs(const LpArgs &a, float (&z)[N], float row_scale, float bias, int t, int t1,
-                                           int row, bool row_in, int lane) {
-    const T *res = static_cast<const T *>(a.residual);
-    T *Y = static_cast<T *>(a.Y);
+// Whole tiles in rounds of all pairs, then the rest, split along K while pairs would idle.
+__device__ __forceinline__ void lp_schedule(LpShared &H, int tiles, int pairs, int nk) {
+    const int rest = tiles % pairs;
+    H.whole = tiles - rest;
+    H.split = rest ? max(1, min(pairs / rest, nk / kLpMinSplit)) : 1;
+    H.units = H.whole + rest * H.split;
+}
+
+// What a chunk of 16 columns (tokens t .. t1 - 1 of them) needs from memory besides its accumulators: the
+// residual of this thread's row, and the tokens' scales, one per lane.  Loaded a chunk ahead.
+template <bool GATED, class T>
+struct LpEnds {
+    static constexpr int N = GATED ? 8 : 16;
+    T res[N];
+    float scale;
+};
+// tokens of a chunk that this thread writes, from its first one: n of them (0 for a row beyond the weight),
+// for a gated weight every other token (lanes 2 i and 2 i + 1 share the outputs of row pair i)
+template <bool GATED>
+__device__ __forceinline__ int lp_count(int t, int t1, bool row_in, int lane) {
+    const int n = row_in ? t1 - t : 0;
+    return GATED ? (n + 1 - (lane & 1)) >> 1 : n;
+}
+template <bool GATED, class T>
+__device__ __forceinline__ void lp_load_ends(const LpArgs &a, LpEnds<GATED, T> &e, int t, int t1, int row, bool row_in, int lane) {
+    if (a.residual) {
+        const int n = lp_count<GATED>(t, t1, row_in, lane);
+        const T *res = static_cast<const T *>(a.residual) + (long long)(t + (GATED ? lane & 1 : 0)) * a.ld_res + (GATED ? row >> 1 : row);
+        const long long step = (GATED ? 2 : 1) * a.ld_res;
+#pragma unroll
+        for (int c = 0; c < LpEnds<GATED, T>::N; c++) {
+            e.res[c] = c < n ? *res : T(0.f);
+            res += step;
+        }
+    }
+    if (a.lin.stage == 2) e.scale = lane < min(16, t1 - t) ? __ldg(a.lin.token_scale + t + lane) : 0.f;
+}
+
+// The outputs of a chunk of this thread's weight row, from its accumulators.  Addresses step from token to
+// token and a count tells which are written: with a comparison and a product per column the code is three
+// times as slow.
+template <bool GATED, class T>
+__device__ __forceinline__ void lp_outputs(const LpArgs &a, float (&z)[16], const LpEnds<GATED, T> &e, float row_scale, float bias,
+                                           int t, int t1, int row, bool row_in, int lane) {
+    constexpr int N = LpEnds<GATED, T>::N;
     if (a.lin.stage == 2) {
 #pragma unroll
-        for (int c = 0; c < N; c++) {
-            const float ts = t + c < t1 ? __ldg(a.lin.token_scale + t + c) : 0.f;
-            z[c] = fmaf(z[c] * row_scale, ts, bias);
-        }
+        for (int c = 0; c < 16; c++) z[c] = fmaf(z[c] * row_scale, __shfl_sync(0xFFFFFFFFu, e.scale, c), bias);
     } else {
 #pragma unroll
-        for (int c = 0; c < N; c++) z[c] = fmaf(z[c], row_scale, bias);
+        for (int c = 0; c < 16; c++) z[c] = fmaf(z[c], row_scale, bias);
     }
+    float y[N];
     if constexpr (GATED) {
         // lanes 2 i and 2 i + 1 hold gate and up of output i: the even lane finishes the even tokens
         const bool up = lane & 1;
-        float g[N / 2], m[N / 2];
+        float m[N];
 #pragma unroll
-        for (int c = 0; c < N / 2; c++) {
+        for (int c = 0; c < N; c++) {
             const float mine = up ? z[2 * c + 1] : z[2 * c];
             const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? z[2 * c] : z[2 * c + 1], 1);
-            g[c] = up ? got : mine;
+            y[c] = up ? got : mine;
             m[c] = up ? mine : got;
         }
-        lin_activate(g, a.act);
-        const long long o = row >> 1;
-        const int tt = t + (int)up;
-        float r[N / 2];
+        lin_activate(y, a.act);
 #pragma unroll
-        for (int c = 0; c < N / 2; c++)
-            r[c] = res && row_in && tt + 2 * c < t1 ? lin_load(res + (long long)(tt + 2 * c) * a.ld_res + o) : 0.f;
-#pragma unroll
-        for (int c = 0; c < N / 2; c++)
-            if (row_in && tt + 2 * c < t1)
-                Y[(long long)(tt + 2 * c) * a.ldy + o] = lin_round<T>(res ? fmaf(g[c], m[c], r[c]) : g[c] * m[c]);
+        for (int c = 0; c < N; c++) y[c] *= m[c];
     } else {
-        lin_activate(z, a.act);
-        if (res) {
-            float r[N];
 #pragma unroll
-            for (int c = 0; c < N; c++) r[c] = row_in && t + c < t1 ? lin_load(res + (long long)(t + c) * a.ld_res + row) : 0.f;
+        for (int c = 0; c < N; c++) y[c] = z[c];
+        lin_activate(y, a.act);
+    }
+    if (a.residual) {
 #pragma unroll
-            for (int c = 0; c < N; c++) z[c] += r[c];
-        }
+        for (int c = 0; c < N; c++) y[c] += lin_float(e.res[c]);
+    }
+    const int n = lp_count<GATED>(t, t1, row_in, lane);
+    T *out = static_cast<T *>(a.Y) + (long long)(t + (GATED ? lane & 1 : 0)) * a.ldy + (GATED ? row >> 1 : row);
+    const long long step = (GATED ? 2 : 1) * a.ldy;
 #pragma unroll
-        for (int c = 0; c < N; c++)
-            if (row_in && t + c < t1) Y[(long long)(t + c) * a.ldy + row] = lin_round<T>(z[c]);
+    for (int c = 0; c < N; c++) {
+        if (c < n) *out = lin_round<T>(y[c]);
+        out += step;
     }
 }
 
@@ -231,7 +276,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     LpShared &H = *reinterpret_cast<LpShared *>(smem_raw + (base - smem_u32(smem_raw)) + kLpStages * kLpStageBytes);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const uint32_t rank = lp_rank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -257,14 +302,22 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&H.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
-    // the decoded weight, the scales, the counters and the restated tokens are the first kernel's
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int rt = (a.lin.rows + kLinRows - 1) / kLinRows;
     if (warp == 0) {
-        int tiles = 0;
-        if (GROUPED) {
+        if (lane < 5) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.w : &maps.x[lane - 1]) : "memory");
+        if (!GROUPED && lane == 0) lp_schedule(H, rt * (int)((a.lin.tokens + kLinTokens - 1) / kLinTokens), pairs, nk);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    lp_cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    // the decoded weight, the scales, the counters and the restated tokens are the first kernel's
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (GROUPED) {
+        if (warp == 0) {
             const int n = max(lin_groups<true>(a.lin, H.id, H.lo, H.hi), 0);
             __syncwarp();
+            int tiles = 0;
             for (int g0 = 0; g0 < n; g0 += 32) {              // tiles before each group
                 const int g = g0 + lane;
                 const int mine = g < n ? rt * ((H.hi[g] - H.lo[g] + kLinTokens - 1) / kLinTokens) : 0;
@@ -277,104 +330,109 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                 if (g < n) H.first[g] = tiles + sum - mine;
                 tiles += __shfl_sync(0xFFFFFFFFu, sum, 31);
             }
-            if (lane == 0) H.nact = n;
-        } else {
-            tiles = rt * (int)((a.lin.tokens + kLinTokens - 1) / kLinTokens);
+            if (lane == 0) {
+                H.nact = n;
+                lp_schedule(H, tiles, pairs, nk);
+            }
         }
-        if (lane == 0) {
-            const int rest = tiles % pairs;
-            H.tiles = tiles;
-            H.whole = tiles - rest;
-            H.split = rest ? max(1, min(pairs / rest, nk / kLpMinSplit)) : 1;
-            H.units = H.whole + rest * H.split;
-        }
+        __syncthreads();
     }
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
-    lp_cluster_sync();
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = H.tmem;
     const int units = H.units;
     volatile int *abort_flag = &H.abort;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- loads of this CTA: its 128 weight rows and its half of the tokens, for the leader's barrier
-            uint32_t it = 0;
-            bool ok = true;
-            for (int u = pair; u < units && ok; u += pairs) {
-                const LpUnit x = lp_unit<GROUPED>(a, H, u, nk);
-                const int half = x.n >> 1;
-                const int wrow = x.group * a.lin.rows + x.row0 + 128 * (int)rank;
-                const int trow = x.t0 + half * (int)rank;
-                for (int k = x.k0; k < x.k1; k++, it++) {
-                    const int s = it % kLpStages;
-                    ok = lp_wait(smem_u32(&H.empty[s]), ((it / kLpStages) & 1u) ^ 1u, tries) && !*abort_flag;
-                    if (!ok) break;
-                    const uint32_t bar = lp_leader(smem_u32(&H.full[s]));
+        // ---- loads of this CTA: its 128 weight rows and its half of the tokens, for the leader's barrier
+        const uint32_t full0 = lp_uniform((int)lp_leader(smem_u32(&H.full[0]))), empty0 = smem_u32(&H.empty[0]);
+        uint32_t s = 0, phase = 1, issued = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += pairs) {
+            const LpUnit x = lp_unit<GROUPED>(a, H, u, nk);
+            const int half = lp_uniform(x.n >> 1), k1 = lp_uniform(x.k1);
+            const int wrow = lp_uniform(x.group * a.lin.rows + x.row0 + 128 * (int)rank);
+            const int trow = lp_uniform(x.t0 + half * (int)rank);
+            const uint32_t bytes = 2u * (uint32_t)(kLpABytes + half * kLpK * 2);
+            for (int k = lp_uniform(x.k0); k < k1; k++) {
+                ok = lp_wait(empty0 + 8 * s, phase, tries);
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                const uint32_t st = base + s * kLpStageBytes, bar = full0 + 8 * s;
+                if (lp_elect()) {
                     if (leader)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                     ::"r"(smem_u32(&H.full[s])), "r"((uint32_t)(2 * (kLpABytes + half * kLpK * 2))) : "memory");
-                    const uint32_t st = base + s * kLpStageBytes;
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
                     lp_load(st, &maps.w, k * kLpK, wrow, bar);
-                    uint32_t at = 0;
+                    if (half == 128) {
+                        lp_load(st + kLpABytes, &maps.x[0], k * kLpK, trow, bar);
+                    } else {
+                        int at = 0;
 #pragma unroll
-                    for (int b = 0; b < 4; b++) {
-                        const int box = 128 >> b;
-                        if (half & box) {
-                            lp_load(st + kLpABytes + at * kLpK * 2, &maps.x[b], k * kLpK, trow + (int)at, bar);
-                            at += box;
+                        for (int b = 1; b < 4; b++) {
+                            if (half & (128 >> b)) {
+                                lp_load(st + kLpABytes + at * kLpK * 2, &maps.x[b], k * kLpK, trow + at, bar);
+                                at += 128 >> b;
+                            }
                         }
                     }
                 }
+                __syncwarp();
+                issued++;
+                if (++s == kLpStages) { s = 0; phase ^= 1u; }
             }
-            // the last products' releases of the stages must have arrived before this CTA may leave
-            for (uint32_t back = min(it, (uint32_t)kLpStages); ok && back > 0; back--) {
-                const uint32_t i = it - back;
-                ok = lp_wait(smem_u32(&H.empty[i % kLpStages]), (i / kLpStages) & 1u, tries);
-            }
-            if (!ok) *abort_flag = 1;
-            // copies still under way after a wait gave up: the leader waits for the last of each stage
-            if (leader && !ok)
-                for (uint32_t back = 1; back <= (uint32_t)kLpStages && back <= it; back++) {
-                    const uint32_t i = it - back;
-                    lp_wait(smem_u32(&H.full[i % kLpStages]), (i / kLpStages) & 1u, kBulkWaitTries);
-                }
         }
+        // the last products' releases of the stages must have arrived before this CTA may leave
+        for (uint32_t back = min(issued, (uint32_t)kLpStages); ok && back > 0; back--) {
+            const uint32_t i = issued - back;
+            ok = lp_wait(empty0 + 8 * (i % kLpStages), (i / kLpStages) & 1u, tries);
+        }
+        if (!ok) *abort_flag = 1;
+        // copies still under way after a wait gave up: the leader waits for the last of each stage
+        if (leader && !ok)
+            for (uint32_t back = 1; back <= min(issued, (uint32_t)kLpStages); back++) {
+                const uint32_t i = issued - back;
+                lp_wait(smem_u32(&H.full[i % kLpStages]), (i / kLpStages) & 1u, kBulkWaitTries);
+            }
     } else if (warp == 1) {
-        if (leader && lane == 0) {
+        if (leader) {
             // ---- products: one thread issues for both CTAs
-            uint32_t it = 0, tile = 0;
+            const uint32_t full0 = smem_u32(&H.full[0]), empty0 = smem_u32(&H.empty[0]);
+            const uint32_t tmem0 = lp_uniform((int)tmem);
+            uint32_t s = 0, phase = 0, tile = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs, tile++) {
                 const LpUnit x = lp_unit<GROUPED>(a, H, u, nk);
                 const uint32_t b = tile & 1u;
                 ok = lp_wait(smem_u32(&H.acc_empty[b]), ((tile >> 1) & 1u) ^ 1u, tries);
-                if (!ok) break;
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t idesc = lp_idesc(x.n), d = tmem + b * kLinTokens;
-                for (int k = x.k0; k < x.k1; k++, it++) {
-                    const int s = it % kLpStages;
-                    ok = lp_wait(smem_u32(&H.full[s]), (it / kLpStages) & 1u, tries) && !*abort_flag;
-                    if (!ok) break;
+                const uint32_t idesc = lp_idesc(lp_uniform(x.n)), d = tmem0 + b * kLinTokens;
+                const int k0 = lp_uniform(x.k0), k1 = lp_uniform(x.k1);
+                for (int k = k0; k < k1; k++) {
+                    ok = lp_wait(full0 + 8 * s, phase, tries);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint64_t ad = lp_desc(base + s * kLpStageBytes), bd = lp_desc(base + s * kLpStageBytes + kLpABytes);
+                    if (lp_elect()) {
 #pragma unroll
-                    for (int q = 0; q < kLpK / 16; q++)       // 16 columns are 32 bytes along the swizzled row
-                        asm volatile(
-                            "{\n\t.reg .pred p;\n\t"
-                            "setp.ne.b32 p, %4, 0;\n\t"
-                            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                            ::"r"(d), "l"(ad + 2 * q), "l"(bd + 2 * q), "r"(idesc), "r"((uint32_t)(k > x.k0 || q > 0)));
-                    lp_commit(smem_u32(&H.empty[s]));
+                        for (int q = 0; q < kLpK / 16; q++)       // 16 columns are 32 bytes along the swizzled row
+                            asm volatile(
+                                "{\n\t.reg .pred p;\n\t"
+                                "setp.ne.b32 p, %4, 0;\n\t"
+                                "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                                ::"r"(d), "l"(ad + 2 * q), "l"(bd + 2 * q), "r"(idesc), "r"((uint32_t)(k > k0 || q > 0)));
+                        lp_commit(empty0 + 8 * s);
+                    }
+                    __syncwarp();
+                    if (++s == kLpStages) { s = 0; phase ^= 1u; }
                 }
-                if (ok) lp_commit(smem_u32(&H.acc_full[b]));
+                if (ok && lp_elect()) lp_commit(smem_u32(&H.acc_full[b]));
+                __syncwarp();
             }
             if (!ok) {
                 // products under way read shared memory and write TMEM: wait for them before leaving
                 *abort_flag = 1;
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                             ::"r"(smem_u32(&H.drain)) : "memory");
+                if (lp_elect())
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                                 ::"r"(smem_u32(&H.drain)) : "memory");
+                __syncwarp();
                 if (!lp_wait(smem_u32(&H.drain), 0, kBulkWaitTries)) *abort_flag = 2;
             }
         }
@@ -402,51 +460,66 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             ok = lp_epilogue_all(ok);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            float *slot = x.split > 1 ? a.partial + ((long long)x.slot * 2 + rank) * kLinTokens * 128 : nullptr;
-            for (int c0 = odd * 32; c0 < x.n; c0 += 64) {
-                uint32_t v[32];
-                lp_tmem_load(tlane + b * kLinTokens + c0, v);
-                if (slot) {
+            // this warp's chunks of 16 columns: every other one
+            const int chunks = (x.t1 - x.t0 + 15) >> 4;
+            const uint32_t acc = tlane + b * kLinTokens;
+            uint32_t mine = 0xFFFFFFFFu;                       // chunks to finish here
+            const float4 *parts = nullptr;
+            if (x.split > 1) {
+                // partial sums to the workspace, four columns of a row together; whichever split of a
+                // chunk arrives last finishes it
+                float4 *own = reinterpret_cast<float4 *>(a.partial) + ((long long)x.slot * 2 + rank) * (kLinTokens * 32) + lrow;
+                for (int c = odd; c < chunks; c += 2) {
+                    float z[16];
+                    lp_tmem_load(acc + 16 * c, z);
 #pragma unroll
-                    for (int c = 0; c < 32; c++) __stcg(slot + (c0 + c) * 128 + lrow, __uint_as_float(v[c]));
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        float z[16];
-#pragma unroll
-                        for (int c = 0; c < 16; c++) z[c] = __uint_as_float(v[16 * h + c]);
-                        if (x.t0 + c0 + 16 * h < x.t1)
-                            lp_outputs<GATED, T>(a, z, rs, bias, x.t0 + c0 + 16 * h, x.t1, row, row_in, lane);
-                    }
+                    for (int i = 0; i < 4; i++)
+                        __stcg(own + (4 * c + i) * 128, make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
                 }
+                __threadfence();
+                __syncwarp();
+                unsigned before = 0;
+                const int c = 2 * lane + odd;
+                if (lane < 8 && c < chunks) before = atomicAdd(a.lin.counters + ((x.tile * 2 + rank) * 4 + quarter) * 16 + c, 1u);
+                mine = __ballot_sync(0xFFFFFFFFu, lane < 8 && before == (unsigned)(x.split - 1));
+                __threadfence();
+                parts = reinterpret_cast<const float4 *>(a.partial) +
+                        ((long long)x.tile * x.split * 2 + rank) * (kLinTokens * 32) + lrow;
+            }
+            mine &= (1u << ((chunks - odd + 1) >> 1)) - 1u;
+            LpEnds<GATED, T> ends;
+            if (mine) lp_load_ends<GATED, T>(a, ends, x.t0 + 16 * (2 * (__ffs(mine) - 1) + odd), x.t1, row, row_in, lane);
+            while (mine) {
+                const int c = 2 * (__ffs(mine) - 1) + odd;
+                mine &= mine - 1u;
+                float z[16];
+                if (x.split > 1) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++) z[i] = 0.f;
+#pragma unroll 4
+                    for (int p = 0; p < x.split; p++) {        // in the order of the splits
+                        const float4 *src = parts + (long long)p * 2 * (kLinTokens * 32) + 4 * c * 128;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float4 q = __ldcg(src + i * 128);
+                            z[4 * i] += q.x;
+                            z[4 * i + 1] += q.y;
+                            z[4 * i + 2] += q.z;
+                            z[4 * i + 3] += q.w;
+                        }
+                    }
+                } else {
+                    lp_tmem_load(acc + 16 * c, z);
+                }
+                const LpEnds<GATED, T> now = ends;
+                if (mine) lp_load_ends<GATED, T>(a, ends, x.t0 + 16 * (2 * (__ffs(mine) - 1) + odd), x.t1, row, row_in, lane);
+                lp_outputs<GATED, T>(a, z, now, rs, bias, x.t0 + 16 * c, x.t1, row, row_in, lane);
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0)
                 asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                              ::"r"(lp_leader(smem_u32(&H.acc_empty[b]))) : "memory");
-            if (x.split > 1) {
-                // this CTA's half of the tile: whoever arrives last adds the splits, in their order
-                __threadfence();
-                lp_epilogue_all(true);
-                if (tid == 64) H.last = atomicAdd(a.lin.counters + x.tile * 2 + rank, 1u) == (unsigned)(x.split - 1);
-                lp_epilogue_all(true);
-                if (H.last) {
-                    __threadfence();
-                    const float *first = a.partial + ((long long)x.tile * x.split * 2 + rank) * kLinTokens * 128;
-                    for (int c0 = odd * 16; c0 < x.n && x.t0 + c0 < x.t1; c0 += 32) {
-                        float z[16];
-#pragma unroll
-                        for (int c = 0; c < 16; c++) z[c] = 0.f;
-                        for (int p = 0; p < x.split; p++) {
-                            const float *src = first + (long long)p * 2 * kLinTokens * 128 + c0 * 128 + lrow;
-#pragma unroll
-                            for (int c = 0; c < 16; c++) z[c] += __ldcg(src + c * 128);
-                        }
-                        lp_outputs<GATED, T>(a, z, rs, bias, x.t0 + c0, x.t1, row, row_in, lane);
-                    }
-                }
-            }
         }
         if (!ok && lane == 0) *abort_flag = 1;
     }
