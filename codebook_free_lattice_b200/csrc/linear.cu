@@ -13,6 +13,7 @@ using namespace llvq;
 namespace {
 
 constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
+constexpr int kDotTokens = 8;
 constexpr long long kMaxRunRows = 0xFFFF;                  // row field of a record
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -38,12 +39,27 @@ struct Plan {
     int stage = 0;                                         // LinArgs::stage
     long long held = 0;                                    // rows of the decoded weight
     long long w_pitch = 0, xs_pitch = 0;
+    bool dots = false;                                     // few tokens: no decoded weight
     size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
 };
 
 llvq_status refuse(const char *why, llvq_status st = LLVQ_ERR_ARG) {
     g_last_error = why;
     return st;
+}
+
+constexpr size_t kSmemLimit = 232448;                      // opt-in shared memory per block on sm_100
+
+size_t dequant_smem(int bits, int out, bool grouped, long long tokens, int nb) {
+    return (bits == 48 ? dq48_fixed() : bits == 72 ? dq_fixed<Dec72>() : dq_fixed<Dec96>()) + dq_tail(out, grouped, tokens, nb);
+}
+int dequant_ctas(int bits) { return bits == 48 ? 1 : bits == 72 ? Dec72::kCtasPerSm : Dec96::kCtasPerSm; }
+
+// Whether a call multiplies its tokens block by block as they are decoded, without a decoded weight: up to
+// kDotTokens tokens whose activations fit in shared memory beside the decoder's tables.
+bool few_tokens(const llvq_codec *c, const llvq_weight *w, int64_t tokens, bool grouped) {
+    return tokens <= kDotTokens &&
+           dequant_smem(c->index_bits, kDqDots, grouped, tokens, w->blocks_per_row) <= kSmemLimit / dequant_ctas(c->index_bits) - 1024;
 }
 
 // Checks a call (everything but the workspace) and lays out its workspace.
@@ -89,6 +105,12 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         at += round256(bytes);
         return here;
     };
+    p.dots = few_tokens(c, w, q->tokens, grouped);
+    if (p.dots) {
+        p.w = place((size_t)q->tokens * p.held * w->blocks_per_row * sizeof(float));
+        p.bytes = at;
+        return LLVQ_OK;
+    }
     p.w = place((size_t)p.held * p.w_pitch * sizeof(__half));
     p.row_scale = place((size_t)p.held * sizeof(float));
     p.counters = place((size_t)c->pairs * kLpCounters * sizeof(unsigned));
@@ -127,9 +149,9 @@ bool make_map(CUtensorMap &m, const void *base, long long rows, long long cols, 
 
 // A launch whose prologue may overlap the end of the kernel before it on the stream.
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t st, A &&...args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A &&...args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -141,8 +163,10 @@ cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <bool GROUPED>
+template <int OUT, bool GROUPED>
 cudaError_t launch_dequant(const llvq_codec *c, const llvq_weight *w, const LinArgs &a, cudaStream_t st) {
+    const size_t smem = dequant_smem(c->index_bits, OUT, GROUPED, a.tokens, a.nb);
+    const int grid = c->num_sms * dequant_ctas(c->index_bits);
     if (c->index_bits == 48) {
         Dq48Args d{};
         d.image = (const SmemGv48 *)c->d_gv48;
@@ -150,23 +174,33 @@ cudaError_t launch_dequant(const llvq_codec *c, const llvq_weight *w, const LinA
         d.tabC = c->d_tabC48;
         d.words = (const unsigned long long *)w->words;
         d.wait_tries = g_first_wait_tries.load();
-        auto kernel = w->gain_mode == LLVQ_GAIN_FP16_DIRECT ? k_dequant48<0, GROUPED> : k_dequant48<1, GROUPED>;
-        return launch(kernel, c->num_sms, kDqThreads, dq48_smem(GROUPED), st, a, d);
+        auto kernel = w->gain_mode == LLVQ_GAIN_FP16_DIRECT ? k_dequant48<OUT, 0, GROUPED> : k_dequant48<OUT, 1, GROUPED>;
+        return launch(kernel, dim3((unsigned)grid), kDqThreads, smem, st, a, d);
     }
     const unsigned long long lo = (unsigned long long)c->npoints, hi = (unsigned long long)(c->npoints >> 64);
     if (c->index_bits == 72) {
         const Dec72::Args d{(const Smem72 *)c->d_image, c->d_recs72, c->d_guide72, lo, hi};
-        return launch(k_dequant<Dec72, GROUPED>, c->num_sms * Dec72::kCtasPerSm, 512, dq_smem<Dec72>(GROUPED), st, a, d,
-                      (const Dec72::Word *)w->words);
+        return launch(k_dequant<Dec72, OUT, GROUPED>, dim3((unsigned)grid), 512, smem, st, a, d, (const Dec72::Word *)w->words);
     }
     const Dec96::Args d{(const Smem96 *)c->d_image, c->d_recs96, c->d_guide96, lo, (uint32_t)hi};
-    return launch(k_dequant<Dec96, GROUPED>, c->num_sms * Dec96::kCtasPerSm, 512, dq_smem<Dec96>(GROUPED), st, a, d,
-                  (const Dec96::Word *)w->words);
+    return launch(k_dequant<Dec96, OUT, GROUPED>, dim3((unsigned)grid), 512, smem, st, a, d, (const Dec96::Word *)w->words);
+}
+
+template <bool GROUPED, bool GATED, class T>
+cudaError_t launch_finish(const LinArgs &a, const DqEnds &e, cudaStream_t st) {
+    const int outs = GATED ? a.half : a.rows;
+    const int blocks = std::min((outs + kDqFinishWarps - 1) / kDqFinishWarps, 4096);
+    return launch(k_linear_finish<GROUPED, GATED, T>, dim3((unsigned)blocks, (unsigned)a.tokens), 32 * kDqFinishWarps, 0, st, a, e);
+}
+template <bool GROUPED>
+cudaError_t finish_dispatch(const LinArgs &a, const DqEnds &e, bool gated, bool bf16, cudaStream_t st) {
+    if (gated) return bf16 ? launch_finish<GROUPED, true, __nv_bfloat16>(a, e, st) : launch_finish<GROUPED, true, __half>(a, e, st);
+    return bf16 ? launch_finish<GROUPED, false, __nv_bfloat16>(a, e, st) : launch_finish<GROUPED, false, __half>(a, e, st);
 }
 
 template <bool GROUPED, bool GATED, class T>
 cudaError_t launch_product(const llvq_codec *c, const LpMaps &m, const LpArgs &a, cudaStream_t st) {
-    return launch(k_linear_product<GROUPED, GATED, T>, 2 * c->pairs, kLpThreads, lp_smem(GROUPED), st, m, a);
+    return launch(k_linear_product<GROUPED, GATED, T>, dim3((unsigned)(2 * c->pairs)), kLpThreads, lp_smem(GROUPED), st, m, a);
 }
 template <bool GROUPED>
 cudaError_t product_dispatch(const llvq_codec *c, const LpMaps &m, const LpArgs &a, bool gated, bool bf16, cudaStream_t st) {
@@ -185,7 +219,6 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes) return refuse("workspace null, misaligned or too small");
     DeviceScope scope(c->device);
     if (!scope.ok) return LLVQ_ERR_CUDA;
-    if (!encode_tiled()) return refuse("the driver has no cuTensorMapEncodeTiled", LLVQ_ERR_CUDA);
     unsigned char *ws = (unsigned char *)workspace;
     LpArgs a{};
     LinArgs &l = a.lin;
@@ -212,7 +245,19 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     l.Xs = (__half *)(ws + p.xs);
     l.ldxs = p.xs_pitch;
     l.token_scale = (float *)(ws + p.token_scale);
+    l.dots = (float *)(ws + p.w);
+    l.held = p.held;
+    l.bf16 = q->dtype == LLVQ_DTYPE_BF16;
     l.flags = c->d_flags;
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool bf16 = l.bf16;
+    if (p.dots) {
+        const DqEnds ends{q->bias, q->residual, q->residual_stride, q->y, q->y_stride, q->activation};
+        cudaError_t e = grouped ? launch_dequant<kDqDots, true>(c, w, l, s) : launch_dequant<kDqDots, false>(c, w, l, s);
+        if (e == cudaSuccess) e = grouped ? finish_dispatch<true>(l, ends, q->gated, bf16, s) : finish_dispatch<false>(l, ends, q->gated, bf16, s);
+        return e == cudaSuccess ? LLVQ_OK : refuse(cudaGetErrorString(e), LLVQ_ERR_CUDA);
+    }
+    if (!encode_tiled()) return refuse("the driver has no cuTensorMapEncodeTiled", LLVQ_ERR_CUDA);
     a.bias = q->bias;
     a.residual = q->residual;
     a.ld_res = q->residual_stride;
@@ -228,9 +273,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;
     for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.cols, pitch, 128 >> b);
     if (!ok) return refuse("sizes or strides beyond a tensor map", LLVQ_ERR_UNSUPPORTED);
-    cudaStream_t s = (cudaStream_t)stream;
-    const bool bf16 = q->dtype == LLVQ_DTYPE_BF16;
-    cudaError_t e = grouped ? launch_dequant<true>(c, w, l, s) : launch_dequant<false>(c, w, l, s);
+    cudaError_t e = grouped ? launch_dequant<kDqWeights, true>(c, w, l, s) : launch_dequant<kDqWeights, false>(c, w, l, s);
     if (e == cudaSuccess)
         e = grouped ? product_dispatch<true>(c, m, a, q->gated, bf16, s) : product_dispatch<false>(c, m, a, q->gated, bf16, s);
     if (e == cudaSuccess) return LLVQ_OK;
@@ -243,10 +286,14 @@ void allow(K kernel, size_t smem) {
 }
 template <bool GROUPED>
 void allow_all() {
-    allow(k_dequant48<0, GROUPED>, dq48_smem(GROUPED));
-    allow(k_dequant48<1, GROUPED>, dq48_smem(GROUPED));
-    allow(k_dequant<Dec72, GROUPED>, dq_smem<Dec72>(GROUPED));
-    allow(k_dequant<Dec96, GROUPED>, dq_smem<Dec96>(GROUPED));
+    allow(k_dequant48<kDqWeights, 0, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqWeights, 1, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqDots, 0, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqDots, 1, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec72, kDqWeights, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec72, kDqDots, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec96, kDqWeights, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec96, kDqDots, GROUPED>, kSmemLimit);
     allow(k_linear_product<GROUPED, false, __half>, lp_smem(GROUPED));
     allow(k_linear_product<GROUPED, true, __half>, lp_smem(GROUPED));
     allow(k_linear_product<GROUPED, false, __nv_bfloat16>, lp_smem(GROUPED));
@@ -256,7 +303,7 @@ void allow_all() {
 }  // namespace
 
 void llvq::set_linear_attrs(llvq_codec *c) {
-    static_assert(dq48_smem(true) <= 232448 && lp_smem(true) <= 232448, "shared memory of an SM");
+    static_assert(dq48_fixed() + dq_tail(kDqWeights, true, 0, 0) <= kSmemLimit && lp_smem(true) <= kSmemLimit, "shared memory of an SM");
     allow_all<false>();
     allow_all<true>();
     // pairs of CTAs that are resident at once, one CTA per SM

@@ -26,6 +26,7 @@ namespace llvq {
 constexpr int kLinExperts = 2048;             // most experts of one call (their groups sit in shared memory)
 constexpr int kLinRows = 256;                 // weight rows of a tile (one pair of CTAs)
 constexpr int kLinTokens = 256;               // most tokens of a tile
+constexpr int kLinDots = 16;                  // most tokens of a call without a decoded weight
 
 struct LinArgs {
     // the layer: `experts` stacked matrices of `rows` rows; half = rows / 2 when gated, else 0
@@ -52,6 +53,10 @@ struct LinArgs {
     __half *Xs;
     long long ldxs;
     float *token_scale;
+    // few tokens: the blocks' dot products [token][row of the decoded weight][nb] instead of the weight
+    float *dots;
+    long long held;                           // rows of the decoded weight
+    int bf16;
     unsigned *flags;
 };
 
@@ -70,10 +75,11 @@ __device__ __forceinline__ int lin_place(int r, int half) {
 }
 
 // The experts that have tokens, in order, by one warp: id[i], and with EDGES their token ranges
-// lo[i], hi[i].  Offsets that fall, start below zero or end beyond the tokens leave no expert (the
-// flag is raised by the caller); returns the count, or -1 for such offsets.
+// lo[i], hi[i]; at most `room` of them are written (offsets in order never leave more than room).  Offsets
+// that fall, start below zero or end beyond the tokens leave no expert (the flag is raised by the
+// caller); returns the count, or -1 for such offsets.
 template <bool EDGES>
-__device__ __forceinline__ int lin_groups(const LinArgs &a, int *id, int *lo, int *hi) {
+__device__ __forceinline__ int lin_groups(const LinArgs &a, int room, int *id, int *lo, int *hi) {
     const int lane = threadIdx.x & 31;
     int n = 0;
     bool bad = false;
@@ -88,10 +94,12 @@ __device__ __forceinline__ int lin_groups(const LinArgs &a, int *id, int *lo, in
         const unsigned m = __ballot_sync(0xFFFFFFFFu, t > s);
         if (t > s) {
             const int i = n + __popc(m & ((1u << lane) - 1u));
-            id[i] = e;
-            if (EDGES) {
-                lo[i] = s;
-                hi[i] = t;
+            if (i < room) {
+                id[i] = e;
+                if (EDGES) {
+                    lo[i] = s;
+                    hi[i] = t;
+                }
             }
         }
         n += __popc(m);
@@ -150,6 +158,31 @@ __device__ __forceinline__ uint4 lin_load8(const uint16_t *row, int i, int n, bo
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// The scale of a bf16 token whose largest finite magnitude has these bits: 2^-u, leaving that value in fp16's
+// top binade (subnormals: exponent -126 stands for all of them; 2^126 is the most its inverse can be).
+__device__ __forceinline__ float lin_token_scale(uint32_t top) {
+    return pow2(top == 0u ? 0 : max(max((int)(top >> 23) - 127, -126) - 14, -126));
+}
+// eight bf16 values scaled to fp16, and their largest finite magnitude
+__device__ __forceinline__ uint4 lin_restate8(uint4 q, float f) {
+    const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(h[k] << 16) * f, __uint_as_float(h[k] & 0xFFFF0000u) * f);
+        o[k] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint32_t lin_top8(uint4 q) {
+    const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        top = max(top, max(finite_bits(__uint_as_float(h[k] << 16)), finite_bits(__uint_as_float(h[k] & 0xFFFF0000u))));
+    return top;
+}
+
 // One token restated for the product, by one warp: fp16 copied to an aligned row (no scale), bf16 scaled by a
 // power of two and rounded to fp16 (see above).  The row is read twice; the second time it is in L1.
 __device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, int cols, float *scale) {
@@ -163,31 +196,12 @@ __device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, in
     }
     uint32_t top = 0;
 #pragma unroll 4
-    for (int i = lane; i < n8; i += 32) {
-        const uint4 q = lin_load8(src, 8 * i, cols, wide);
-        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            top = max(top, max(finite_bits(__uint_as_float(h[k] << 16)), finite_bits(__uint_as_float(h[k] & 0xFFFF0000u))));
-    }
+    for (int i = lane; i < n8; i += 32) top = max(top, lin_top8(lin_load8(src, 8 * i, cols, wide)));
     top = warp_max(top);
-    // the largest value's exponent (subnormals: -126 stands for all of them); 2^126 is the most a
-    // scale's inverse can be
-    const int ex = max((int)(top >> 23) - 127, -126);
-    const float inv = pow2(top == 0u ? 0 : max(ex - 14, -126)), f = pow2_inverse(inv);
+    const float inv = lin_token_scale(top), f = pow2_inverse(inv);
     if (lane == 0) *scale = inv;
 #pragma unroll 4
-    for (int i = lane; i < n8; i += 32) {
-        const uint4 q = lin_load8(src, 8 * i, cols, wide);
-        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const __half2 v = __floats2half2_rn(__uint_as_float(h[k] << 16) * f, __uint_as_float(h[k] & 0xFFFF0000u) * f);
-            o[k] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    for (int i = lane; i < n8; i += 32) dst[i] = lin_restate8(lin_load8(src, 8 * i, cols, wide), f);
 }
 
 // Activations, four values at a time and out of line: the code of one activation is fetched once, and

@@ -1,5 +1,6 @@
 // linear_dequant.cuh -- the first kernel of a compressed linear layer: every block of the experts
-// that have tokens is decoded once and written as 24 scaled fp16 weights (linear_common.cuh).
+// that have tokens is decoded once, and written as 24 scaled fp16 weights (linear_common.cuh) or, for a few
+// tokens, multiplied with them at once (k_linear_finish then adds each row's dot products in order).
 //
 // "Leech Lattice Vector Quantization for Efficient LLM Compression", papernotes.org notes,
 // 方法详解 / 关键设计 2: index -> shell, class, codeword, signs, arrangement -> integer vector.
@@ -25,15 +26,23 @@ struct DqShared {
     int slice_next, stage_next, nact, pad;
     unsigned long long bar;
     unsigned long long pad2;
-    int id[kLinExperts];
+    int left[2][32], head[2][32];             // what the rings hold at the end, and where
+    int id[kLinExperts];                      // the active experts (weights), or DqDots in this place (dots)
 };
-__host__ __device__ constexpr size_t dq48_smem(bool grouped) {
-    return sizeof(SmemGv48) + sizeof(DqRec) * (kDqWarps * 2 * kDqRing) + (grouped ? sizeof(DqShared) : 32);
+// Few tokens: the activations as fp16, one row of nb * 24 values per token (zero beyond the columns), follow.
+struct DqDots {
+    int id[kLinDots], lo[kLinDots], hi[kLinDots];
+    uint32_t top[kLinDots];
+    float scale[kLinDots];
+};
+enum DqOut { kDqWeights = 0, kDqDots = 1 };
+constexpr size_t kDqHead = 32 + 4 * 32 * sizeof(int);              // DqShared without its list
+__host__ __device__ constexpr size_t dq_tail(int out, bool grouped, long long tokens, int nb) {
+    return kDqHead + (out == kDqDots ? sizeof(DqDots) + (size_t)tokens * nb * 48 : grouped ? sizeof(int) * kLinExperts : 0);
 }
+__host__ __device__ constexpr size_t dq48_fixed() { return sizeof(SmemGv48) + sizeof(DqRec) * (kDqWarps * 2 * kDqRing); }
 template <class D>
-__host__ __device__ constexpr size_t dq_smem(bool grouped) {
-    return (sizeof(typename D::Smem) + 15) / 16 * 16 + (grouped ? sizeof(DqShared) : 32);
-}
+__host__ __device__ constexpr size_t dq_fixed() { return (sizeof(typename D::Smem) + 15) / 16 * 16; }
 
 // The run of blocks of one CTA, counted through the active experts' rows in order.
 struct DqRun {
@@ -95,23 +104,106 @@ __device__ __forceinline__ void dq_store_zero(__half *out) {
     p[0] = p[1] = p[2] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// What a CTA does before its blocks: the group list, the counters of the product, its rows' scales.
-// Ends with the scales written (a barrier must follow before they are read).
-template <bool GROUPED>
+// A block's dot products with the tokens of its expert, from shared memory: 24 exact products each, fp32 sums.
+__device__ __forceinline__ void dq_dots(const LinArgs &a, const DqDots &D, const uint32_t wh[12], float scale, int t0, int t1,
+                                        long long row, int j) {
+    const uint4 *x = reinterpret_cast<const uint4 *>(&D + 1) + 3 * j;
+    for (int t = t0; t < t1; t++) {
+        const uint4 *xt = x + 3 * t * a.nb;
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 3; c++) {
+            const uint4 q = xt[c];
+            d0 = fma2_f16_f32(wh[4 * c + 0], q.x, d0);
+            d1 = fma2_f16_f32(wh[4 * c + 1], q.y, d1);
+            d0 = fma2_f16_f32(wh[4 * c + 2], q.z, d0);
+            d1 = fma2_f16_f32(wh[4 * c + 3], q.w, d1);
+        }
+        a.dots[((long long)t * a.held + row) * a.nb + j] = scale * (d0 + d1) * D.scale[t];
+    }
+}
+
+// What becomes of a decoded block (12 exact fp16 pairs; its gain, over |v| for table gains).
+template <int OUT, int GAIN, bool GROUPED>
+__device__ __forceinline__ void dq_block(const LinArgs &a, const DqShared &H, const uint32_t wh[12], float scale, int active,
+                                         long long dst, int j) {
+    if constexpr (OUT == kDqWeights) {
+        dq_store<GAIN>(wh, scale * pow2_inverse(a.row_scale[dst]), a.W + dst * a.ldw + j * 24);
+    } else {
+        const DqDots &D = *reinterpret_cast<const DqDots *>(H.id);
+        const int e = GROUPED ? (int)div_by((uint32_t)active, (uint32_t)a.rows, a.rows_recip) : 0;
+        dq_dots(a, D, wh, scale, GROUPED ? D.lo[e] : 0, GROUPED ? D.hi[e] : (int)a.tokens, dst, j);
+    }
+}
+// ... and of a block whose index is not coded
+template <int OUT, bool GROUPED>
+__device__ __forceinline__ void dq_no_block(const LinArgs &a, const DqShared &H, int active, long long dst, int j) {
+    if constexpr (OUT == kDqWeights) {
+        dq_store_zero(a.W + dst * a.ldw + j * 24);
+    } else {
+        const uint32_t none[12] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        dq_block<OUT, 0, GROUPED>(a, H, none, 0.f, active, dst, j);
+    }
+}
+
+// The activations of a call of few tokens, in this CTA's shared memory, by all its threads; bf16 values
+// with a power of two per token (as in lin_stage_token).  A barrier must follow.
+__device__ __forceinline__ void dq_stage_dots(const LinArgs &a, DqDots &D) {
+    uint4 *x = reinterpret_cast<uint4 *>(&D + 1);
+    const int n8 = 3 * a.nb;                  // 16-byte units of a token
+    const int total = (int)a.tokens * n8;
+    auto load = [&](int i, int &t) {
+        t = i / n8;
+        const uint16_t *src = static_cast<const uint16_t *>(a.X) + t * a.ldx;
+        return lin_load8(src, 8 * (i - t * n8), a.cols, ((unsigned long long)src & 15ull) == 0ull);
+    };
+    if (!a.bf16) {
+        for (int i = threadIdx.x; i < total; i += blockDim.x) {
+            int t;
+            x[i] = load(i, t);
+        }
+        if (threadIdx.x < kLinDots) D.scale[threadIdx.x] = 1.f;
+        return;
+    }
+    if (threadIdx.x < kLinDots) D.top[threadIdx.x] = 0u;
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+        int t;
+        const uint32_t top = lin_top8(load(i, t));
+        if (top > D.top[t]) atomicMax(&D.top[t], top);
+    }
+    __syncthreads();
+    if (threadIdx.x < a.tokens) D.scale[threadIdx.x] = lin_token_scale(D.top[threadIdx.x]);
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+        int t;
+        const uint4 q = load(i, t);
+        x[i] = lin_restate8(q, pow2_inverse(lin_token_scale(D.top[t])));
+    }
+}
+
+// What a CTA does before its blocks: the group list, then the counters of the product and its rows' scales, or
+// the activations of a call of few tokens.  A barrier must follow.
+template <int OUT, bool GROUPED>
 __device__ __forceinline__ DqRun dq_begin(const LinArgs &a, DqShared &H) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int nact = 1;
     if (GROUPED) {
         if (warp == 0) {
-            const int n = lin_groups<false>(a, H.id, nullptr, nullptr);
+            DqDots &D = *reinterpret_cast<DqDots *>(H.id);
+            const int n = OUT == kDqDots ? lin_groups<true>(a, kLinDots, D.id, D.lo, D.hi)
+                                         : lin_groups<false>(a, kLinExperts, H.id, nullptr, nullptr);
             if (lane == 0) H.nact = max(n, 0);
             if (n < 0 && lane == 0 && blockIdx.x == 0) atomicOr(a.flags, LLVQ_FLAG_OFFSETS);
         }
         __syncthreads();
         nact = H.nact;
     }
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x) a.counters[i] = 0u;
     const DqRun run = dq_run(a, nact);
+    if constexpr (OUT == kDqDots) {
+        dq_stage_dots(a, *reinterpret_cast<DqDots *>(H.id));
+        return run;
+    }
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x) a.counters[i] = 0u;
     for (int i = warp; i < run.nrows; i += warps) {
         long long src, dst;
         dq_row<GROUPED>(a, H.id, run.row0 + i, src, dst);
@@ -151,18 +243,17 @@ struct Dq48Args {
     uint32_t wait_tries;
 };
 
-// Decode a record of the given kind (0 odd fast path, 1 even table path, 2 rare) and write it.
-template <int KIND, int GAIN, bool GROUPED>
-__device__ __forceinline__ void dq48_consume(const LinArgs &a, const SmemGv48 &S, const int *id, const DqRec e, int row0) {
+// Decode a record of the given kind (0 odd fast path, 1 even table path, 2 rare) and pass the block on.
+template <int KIND, int OUT, int GAIN, bool GROUPED>
+__device__ __forceinline__ void dq48_consume(const LinArgs &a, const SmemGv48 &S, const DqShared &H, const DqRec e, int row0) {
     const int cls = (int)(e.y & 0x1FFu);
     const uint32_t r = (e.y >> 9) & 0xFFFu;
     const uint32_t info = S.c_info[cls];
-    const int j = (int)(e.w >> 16);
+    const int j = (int)(e.w >> 16), active = row0 + (int)(e.w & 0xFFFFu);
     long long src, dst;
-    dq_row<GROUPED>(a, id, row0 + (int)(e.w & 0xFFFFu), src, dst);
-    const float f = pow2_inverse(a.row_scale[dst]);
-    const float scale = f * (GAIN == 0 ? __half2float(__ldg(a.gains + src * a.nb + j))
-                                       : __half2float(__ldg(a.gains + src * 256 + (e.z >> 24))) * S.invnorm[info_m(info)]);
+    dq_row<GROUPED>(a, H.id, active, src, dst);
+    const float scale = GAIN == 0 ? __half2float(__ldg(a.gains + src * a.nb + j))
+                                  : __half2float(__ldg(a.gains + src * 256 + (e.z >> 24))) * S.invnorm[info_m(info)];
     const unsigned long long p = (unsigned long long)((e.y >> 21) & 1u) << 32 | e.x;
     uint32_t wh[12];
     if constexpr (KIND == 0) {
@@ -177,10 +268,10 @@ __device__ __forceinline__ void dq48_consume(const LinArgs &a, const SmemGv48 &S
 #pragma unroll
         for (int q = 0; q < 6; q++) i8x4_to_h2x2(v[q], wh[2 * q], wh[2 * q + 1]);
     }
-    dq_store<GAIN>(wh, scale, a.W + dst * a.ldw + j * 24);
+    dq_block<OUT, GAIN, GROUPED>(a, H, wh, scale, active, dst, j);
 }
 
-template <int GAIN, bool GROUPED>
+template <int OUT, int GAIN, bool GROUPED>
 __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args d) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SmemGv48 &S = *reinterpret_cast<SmemGv48 *>(smem_raw);
@@ -203,13 +294,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         bulk_load_issue(dst, src, bytes, &H.bar);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const DqRun run = dq_begin<GROUPED>(a, H);
+    const DqRun run = dq_begin<OUT, GROUPED>(a, H);
     if (!bulk_load_wait(&H.bar, d.wait_tries)) {
         if (tid == 0) atomicOr(a.flags, LLVQ_FLAG_WAIT_TIMEOUT);
         return;
     }
     // odd warps restate tokens (memory latency) while the even ones decode (instruction issue)
-    if (warp & 1) dq_stage<GROUPED>(a, H);
+    if (OUT == kDqWeights && (warp & 1)) dq_stage<GROUPED>(a, H);
 
     const int nb = a.nb, total = run.total, nslices = (total + 31) / 32;
     const bool dense = a.word_pitch == (long long)nb && !GROUPED;
@@ -237,11 +328,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         et += __popc(me);
         __syncwarp();
         if (ot - oh >= 32) {
-            dq48_consume<0, GAIN, GROUPED>(a, S, H.id, ring_odd[(oh + lane) & (kDqRing - 1)], run.row0);
+            dq48_consume<0, OUT, GAIN, GROUPED>(a, S, H, ring_odd[(oh + lane) & (kDqRing - 1)], run.row0);
             oh += 32;
         }
         if (et - eh >= 32) {
-            dq48_consume<1, GAIN, GROUPED>(a, S, H.id, ring_even[(eh + lane) & (kDqRing - 1)], run.row0);
+            dq48_consume<1, OUT, GAIN, GROUPED>(a, S, H, ring_even[(eh + lane) & (kDqRing - 1)], run.row0);
             eh += 32;
         }
         __syncwarp();
@@ -272,12 +363,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
             rec.x = __ldg(d.tabC + (S.c_offs[cl.cls] & 0x7FFFFu) + pC);
             rec.y = (uint32_t)cl.cls | cl.r << 9 | pS << 21;
         }
-        if (kind == 2) dq48_consume<2, GAIN, GROUPED>(a, S, H.id, rec, run.row0);
-        if (valid && !cl.ok) {                // an index beyond the coded points: a zero block
+        if (kind == 2) dq48_consume<2, OUT, GAIN, GROUPED>(a, S, H, rec, run.row0);
+        if (valid && !cl.ok) {                // an index beyond the coded points: nothing
             bad = true;
             long long src, dst;
             dq_row<GROUPED>(a, H.id, run.row0 + (int)rl, src, dst);
-            dq_store_zero(a.W + dst * a.ldw + (b - rl * (uint32_t)nb) * 24);
+            dq_no_block<OUT, GROUPED>(a, H, run.row0 + (int)rl, dst, (int)(b - rl * (uint32_t)nb));
         }
         append(prec, pk);
         prec = rec;
@@ -286,14 +377,44 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         sl = sn;
     }
     append(prec, pk);
-    if (lane < ot - oh) dq48_consume<0, GAIN, GROUPED>(a, S, H.id, ring_odd[(oh + lane) & (kDqRing - 1)], run.row0);
-    if (lane < et - eh) dq48_consume<1, GAIN, GROUPED>(a, S, H.id, ring_even[(eh + lane) & (kDqRing - 1)], run.row0);
-    dq_stage<GROUPED>(a, H);
+    // What is left in the rings (fewer than 32 records each) is pooled over the CTA, again in whole warps:
+    // a short run would otherwise spend a fifth of its time on half-empty warps.  Record i of the pool
+    // is found by the rings' cumulative counts.
+    H.left[0][warp] = ot - oh;
+    H.left[1][warp] = et - eh;
+    H.head[0][warp] = oh & (kDqRing - 1);
+    H.head[1][warp] = eh & (kDqRing - 1);
+    __syncthreads();
+    for (int kind = 0; kind < 2; kind++) {
+        int upto = H.left[kind][lane];                       // ring `lane`'s count, then the counts up to it
+        const int mine = upto;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        // warps take the even records from the other end, so that a warp rarely gets a batch of both
+        for (int i0 = 32 * (kind == 0 ? warp : kDqWarps - 1 - warp); i0 < all; i0 += 32 * kDqWarps) {
+            const int i = min(i0 + lane, all - 1);
+            int ring = 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)                 // the first ring whose count up to it is beyond i
+                if (__shfl_sync(0xFFFFFFFFu, upto, ring + o - 1) <= i) ring += o;
+            const int at = i - __shfl_sync(0xFFFFFFFFu, upto - mine, ring) + H.head[kind][ring];
+            const DqRec rec = rings[(2 * ring + kind) * kDqRing + (at & (kDqRing - 1))];
+            if (i0 + lane < all) {
+                if (kind == 0) dq48_consume<0, OUT, GAIN, GROUPED>(a, S, H, rec, run.row0);
+                else dq48_consume<1, OUT, GAIN, GROUPED>(a, S, H, rec, run.row0);
+            }
+        }
+    }
+    if (OUT == kDqWeights) dq_stage<GROUPED>(a, H);
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.flags, LLVQ_FLAG_INDEX_RANGE);
 }
 
 // 72- and 96-bit blocks: one block per thread at a time, the generic decoders.
-template <class D, bool GROUPED>
+template <class D, int OUT, bool GROUPED>
 __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typename D::Args d,
                                                                const typename D::Word *__restrict__ words) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -303,9 +424,9 @@ __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typen
     if (threadIdx.x == 0) H.stage_next = 0;
     load_smem_image(&S, d.image, sizeof(typename D::Smem));
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const DqRun run = dq_begin<GROUPED>(a, H);
+    const DqRun run = dq_begin<OUT, GROUPED>(a, H);
     __syncthreads();
-    dq_stage<GROUPED>(a, H);
+    if (OUT == kDqWeights) dq_stage<GROUPED>(a, H);
     bool bad = false;
     for (int t = threadIdx.x; t < run.total; t += blockDim.x) {
         const uint32_t b = (uint32_t)(run.first + t), rl = div_by(b, (uint32_t)a.nb, a.nb_recip);
@@ -319,13 +440,71 @@ __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typen
         bad |= !ok;
 #pragma unroll
         for (int q = 0; q < 6; q++) i8x4_to_h2x2(ok ? v[q] : 0u, wh[2 * q], wh[2 * q + 1]);
-        const float f = pow2_inverse(a.row_scale[dst]);
-        __half *out = a.W + dst * a.ldw + j * 24;
-        if (!ok) dq_store_zero(out);
-        else if (a.gain_mode == 0) dq_store<0>(wh, f * __half2float(__ldg(a.gains + src * a.nb + j)), out);
-        else dq_store<1>(wh, f * (__half2float(__ldg(a.gains + src * 256 + D::gain_code(w))) * D::invnorm(S, m)), out);
+        const int active = run.row0 + (int)rl;
+        if (!ok) dq_no_block<OUT, GROUPED>(a, H, active, dst, j);
+        else if (a.gain_mode == 0) dq_block<OUT, 0, GROUPED>(a, H, wh, __half2float(__ldg(a.gains + src * a.nb + j)), active, dst, j);
+        else dq_block<OUT, 1, GROUPED>(a, H, wh, __half2float(__ldg(a.gains + src * 256 + D::gain_code(w))) * D::invnorm(S, m), active, dst, j);
     }
     if (__any_sync(0xFFFFFFFFu, bad) && (threadIdx.x & 31) == 0) atomicOr(a.flags, LLVQ_FLAG_INDEX_RANGE);
+}
+
+// The second kernel of a call of few tokens: one warp per output adds the dot products of its row (or gate and
+// up rows), lane by lane and then across the lanes, always in the same order, and applies the epilogue.
+// Bound by its latency: 2.8 MB are read for a 4096 x 4104 layer and one token.
+struct DqEnds {
+    const void *bias, *residual;
+    long long ld_res;
+    void *Y;
+    long long ldy;
+    int act;
+};
+constexpr int kDqFinishWarps = 8;
+template <bool GROUPED, bool GATED, class T>
+__global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a, DqEnds q) {
+    __shared__ int id[kLinDots], lo[kLinDots], hi[kLinDots], count;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (GROUPED) {
+        if (warp == 0) {
+            const int n = lin_groups<true>(a, kLinDots, id, lo, hi);
+            if (lane == 0) count = n;
+        }
+        __syncthreads();
+        if (count < 1) return;
+    }
+    const int outs = GATED ? a.half : a.rows;
+    const int t = blockIdx.y;
+    int e = 0, expert = 0;
+    if (GROUPED) {
+        while (e < count && hi[e] <= t) e++;
+        if (e == count || t < lo[e]) return;
+        expert = id[e];
+    }
+    for (int o = blockIdx.x * kDqFinishWarps + warp; o < outs; o += gridDim.x * kDqFinishWarps) {
+        const float *row = a.dots + ((long long)t * a.held + (long long)e * a.rows + (GATED ? 2 * o : o)) * a.nb;
+        float z = 0.f, up = 0.f;
+        for (int j = lane; j < a.nb; j += 32) {
+            z += __ldcg(row + j);
+            if (GATED) up += __ldcg(row + a.nb + j);
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) {
+            z += __shfl_xor_sync(0xFFFFFFFFu, z, s);
+            if (GATED) up += __shfl_xor_sync(0xFFFFFFFFu, up, s);
+        }
+        if (lane == 0) {
+            if (q.bias) {
+                const T *b = static_cast<const T *>(q.bias) + (long long)expert * a.rows + o;
+                z += lin_load(b);
+                if (GATED) up += lin_load(b + a.half);
+            }
+            float y = q.act == kActNone ? z : lin_activate1(z, q.act);
+            if (GATED) y *= up;
+            if (q.residual) y += lin_load(static_cast<const T *>(q.residual) + t * q.ld_res + o);
+            static_cast<T *>(q.Y)[t * q.ldy + o] = lin_round<T>(y);
+        }
+    }
 }
 
 }  // namespace llvq

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (GROUPED) {
         if (warp == 0) {
-            const int n = max(lin_groups<true>(a.lin, H.id, H.lo, H.hi), 0);
+            const int n = max(lin_groups<true>(a.lin, kLinExperts, H.id, H.lo, H.hi), 0);
             __syncwarp();
             int tiles = 0;
             for (int g0 = 0; g0 < n; g0 += 32) {              // tiles before each group
