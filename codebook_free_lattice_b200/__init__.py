@@ -277,43 +277,60 @@ class Codec:
                             gated, residual, workspace, stream)
 
     def _linear(self, call, name, w, experts, x, offsets, y, bias, activation, gated, residual, workspace, stream):
+        # one pass over each tensor's type, place and layout: this runs on the host for every call
         import torch
-        dtype, rows = x.dtype, w.rows // max(experts, 1)
-        outs = rows // 2 if gated else rows
-        if dtype not in (torch.float16, torch.bfloat16):
+        dtype, on = x.dtype, self.device.index
+        if dtype is not torch.float16 and dtype is not torch.bfloat16:
             raise TypeError(f"{name}: x is {dtype}, not float16 or bfloat16")
-        tokens = x.shape[0] if x.dim() == 2 else -1
-        if x.shape[-1] != w.cols or tokens < 0:
+        outs = w.rows // experts if experts > 1 else w.rows
+        if gated:
+            outs //= 2
+        if x.dim() != 2 or x.shape[1] != w.cols:
             raise ValueError(f"{name}: x is {tuple(x.shape)}, not [tokens, {w.cols}]")
-        for what, t, kind, shape in (("x", x, dtype, None), ("y", y, dtype, (tokens, outs)), ("bias", bias, dtype, None),
-                                     ("residual", residual, dtype, None), ("offsets", offsets, torch.int32, (experts + 1,))):
-            if t is None:
-                continue
-            if t.dtype != kind or t.device != self.device:
-                raise TypeError(f"{name}: {what} is {t.dtype} on {t.device}, not {kind} on {self.device}")
-            if shape is not None and t.shape != shape:
-                raise ValueError(f"{name}: {what} is {tuple(t.shape)}, not {shape}")
-            if t.shape[-1] > 1 and t.stride(-1) != 1:
-                raise ValueError(f"{name}: {what} has a stride of {t.stride(-1)} within its rows")
-        if bias is not None and (bias.numel() != w.rows or not bias.is_contiguous()):
-            raise ValueError(f"{name}: bias is {tuple(bias.shape)}, not {w.rows} contiguous values")
+        tokens = x.shape[0]
+        if y.shape != (tokens, outs):
+            raise ValueError(f"{name}: y is {tuple(y.shape)}, not {(tokens, outs)}")
+        if y.dtype is not dtype or x.get_device() != on or y.get_device() != on:
+            raise TypeError(f"{name}: x is {dtype} on {x.device}, y {y.dtype} on {y.device}; the codec is on {self.device}")
+        (x_stride, x_step), (y_stride, y_step) = x.stride(), y.stride()
+        if (x_step != 1 and w.cols > 1) or (y_step != 1 and outs > 1):
+            raise ValueError(f"{name}: strides of {x_step} (x) and {y_step} (y) within a row, not 1")
+        bias_ptr = res_ptr = off_ptr = None
         res_stride = 0
+        if bias is not None:
+            if bias.dtype is not dtype or bias.get_device() != on:
+                raise TypeError(f"{name}: bias is {bias.dtype} on {bias.device}, not {dtype} on {self.device}")
+            if bias.numel() != w.rows or not bias.is_contiguous():
+                raise ValueError(f"{name}: bias is {tuple(bias.shape)}, not {w.rows} contiguous values")
+            bias_ptr = bias.data_ptr()
         if residual is not None:
+            if residual.dtype is not dtype or residual.get_device() != on:
+                raise TypeError(f"{name}: residual is {residual.dtype} on {residual.device}, not {dtype} on {self.device}")
             if residual.shape not in ((tokens, outs), (1, outs), (outs,)):
                 raise ValueError(f"{name}: residual is {tuple(residual.shape)}, not {(tokens, outs)}")
-            res_stride = residual.stride(0) if residual.dim() == 2 and residual.shape[0] == tokens else 0
+            if outs > 1 and residual.stride(-1) != 1:
+                raise ValueError(f"{name}: a stride of {residual.stride(-1)} within a row of residual, not 1")
+            if residual.dim() == 2 and residual.shape[0] == tokens:
+                res_stride = residual.stride(0)
+            res_ptr = residual.data_ptr()
+        if offsets is not None:
+            if offsets.dtype is not torch.int32 or offsets.get_device() != on:
+                raise TypeError(f"{name}: offsets are {offsets.dtype} on {offsets.device}, not int32 on {self.device}")
+            if offsets.shape != (experts + 1,) or not offsets.is_contiguous():
+                raise ValueError(f"{name}: offsets are {tuple(offsets.shape)}, not {experts + 1} contiguous values")
+            off_ptr = offsets.data_ptr()
         q = llvq_linear_call(tokens, LLVQ_DTYPE_FP16 if dtype is torch.float16 else LLVQ_DTYPE_BF16, activation,
-                             1 if gated else 0, experts, x.data_ptr(), x.stride(0),
-                             None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
-                             res_stride, y.data_ptr(), y.stride(0), None if offsets is None else offsets.data_ptr())
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        need = lib().llvq_linear_workspace(self._h, C.byref(w), C.byref(q))
+                             1 if gated else 0, experts, x.data_ptr(), x_stride, bias_ptr, res_ptr, res_stride,
+                             y.data_ptr(), y_stride, off_ptr)
+        L, wp, qp = lib(), C.byref(w), C.byref(q)
+        raw = torch._C._cuda_getCurrentRawStream(on) if stream is None else stream.cuda_stream
+        need = L.llvq_linear_workspace(self._h, wp, qp)
         if workspace is None or workspace.numel() < need:
-            with torch.cuda.stream(stream):            # the allocator then knows whose memory it is
-                workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=self.device)
-        _check(call(self._h, C.byref(w), C.byref(q), C.c_void_p(workspace.data_ptr()), workspace.numel(),
-                    C.c_void_p(stream.cuda_stream)), name)
+            with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        elif workspace.get_device() != on or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+            raise TypeError(f"{name}: workspace is {workspace.dtype} on {workspace.device}, not contiguous uint8 on {self.device}")
+        _check(call(self._h, wp, qp, workspace.data_ptr(), workspace.numel(), raw), name)
         return workspace
 
     def get_error(self, stream=None) -> int:

@@ -13,7 +13,6 @@ using namespace llvq;
 namespace {
 
 constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
-constexpr int kDotTokens = 8;
 constexpr long long kMaxRunRows = 0xFFFF;                  // row field of a record
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -55,10 +54,14 @@ size_t dequant_smem(int bits, int out, bool grouped, long long tokens, int nb) {
 }
 int dequant_ctas(int bits) { return bits == 48 ? 1 : bits == 72 ? Dec72::kCtasPerSm : Dec96::kCtasPerSm; }
 
-// Whether a call multiplies its tokens block by block as they are decoded, without a decoded weight: up to
-// kDotTokens tokens whose activations fit in shared memory beside the decoder's tables.
-bool few_tokens(const llvq_codec *c, const llvq_weight *w, int64_t tokens, bool grouped) {
-    return tokens <= kDotTokens &&
+// Whether a call multiplies its tokens block by block as they are decoded (no decoded weight, no tile
+// product).  Every further token of an expert costs such a call 3.6 ps per block, the other form about 10 us
+// and 48 written bytes per block once: on one matrix of 4096 x 4096, 1 / 2 / 3 / 4 tokens take 29.6 / 32.7 / 35.5 /
+// 38.7 us against 39.2, on 22016 x 4096 three 141 against 148 and four 159.  Over experts what counts is how many
+// tokens one gets: at most one on average (8 tokens, 8 experts of 2816 x 2048: 55 us against 58; over 4 experts 44
+// against 42).  The activations have to fit in shared memory beside the decoder's tables.
+bool few_tokens(const llvq_codec *c, const llvq_weight *w, int64_t tokens, int experts, bool grouped) {
+    return tokens <= std::max(3, std::min(experts, kLinDots)) &&
            dequant_smem(c->index_bits, kDqDots, grouped, tokens, w->blocks_per_row) <= kSmemLimit / dequant_ctas(c->index_bits) - 1024;
 }
 
@@ -105,7 +108,7 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         at += round256(bytes);
         return here;
     };
-    p.dots = few_tokens(c, w, q->tokens, grouped);
+    p.dots = few_tokens(c, w, q->tokens, p.experts, grouped);
     if (p.dots) {
         p.w = place((size_t)q->tokens * p.held * w->blocks_per_row * sizeof(float));
         p.bytes = at;
