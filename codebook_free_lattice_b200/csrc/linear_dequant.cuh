@@ -182,11 +182,11 @@ __device__ __forceinline__ void dq_stage_dots(const LinArgs &a, DqDots &D) {
     }
 }
 
-// What a CTA does before its blocks: the group list, then the counters of the product and its rows' scales, or
-// the activations of a call of few tokens.  A barrier must follow.
+// What a CTA does before its blocks: the group list and its run; then the counters of the product and its rows'
+// scales, or the activations of a call of few tokens (a barrier must follow).
 template <int OUT, bool GROUPED>
-__device__ __forceinline__ DqRun dq_begin(const LinArgs &a, DqShared &H) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ DqRun dq_groups(const LinArgs &a, DqShared &H) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int nact = 1;
     if (GROUPED) {
         if (warp == 0) {
@@ -199,10 +199,14 @@ __device__ __forceinline__ DqRun dq_begin(const LinArgs &a, DqShared &H) {
         __syncthreads();
         nact = H.nact;
     }
-    const DqRun run = dq_run(a, nact);
+    return dq_run(a, nact);
+}
+template <int OUT, bool GROUPED>
+__device__ __forceinline__ void dq_begin(const LinArgs &a, DqShared &H, const DqRun &run) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     if constexpr (OUT == kDqDots) {
         dq_stage_dots(a, *reinterpret_cast<DqDots *>(H.id));
-        return run;
+        return;
     }
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x) a.counters[i] = 0u;
     for (int i = warp; i < run.nrows; i += warps) {
@@ -211,7 +215,6 @@ __device__ __forceinline__ DqRun dq_begin(const LinArgs &a, DqShared &H) {
         const float s = lin_row_scale(a, src);
         if (lane == 0) a.row_scale[dst] = s;       // a row shared with the next CTA gets the same value twice
     }
-    return run;
 }
 
 // The tokens a CTA restates: every gridDim.x-th of the tokens in use, one warp per token.
@@ -295,14 +298,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         bulk_load_issue(dst, src, bytes, &H.bar);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const DqRun run = dq_begin<OUT, GROUPED>(a, H);
-    if (!bulk_load_wait(&H.bar, d.wait_tries)) {
-        if (tid == 0) atomicOr(a.flags, LLVQ_FLAG_WAIT_TIMEOUT);
-        return;
-    }
-    // odd warps restate tokens (memory latency) while the even ones decode (instruction issue)
-    if (OUT == kDqWeights && (warp & 1)) dq_stage<GROUPED>(a, H);
-
+    const DqRun run = dq_groups<OUT, GROUPED>(a, H);
     const int nb = a.nb, total = run.total, nslices = (total + 31) / 32;
     const bool dense = a.word_pitch == (long long)nb && !GROUPED;
     const unsigned long long *wfirst = d.words + (long long)run.row0 * nb + run.first;     // dense only
@@ -320,6 +316,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         if (t < total) asm volatile("prefetch.global.L2 [%0];" ::"l"(word_at(t)));
     };
     if (tid < 2 * (kDqWarps + kDqAhead)) prefetch(16 * tid);
+
+    dq_begin<OUT, GROUPED>(a, H, run);
+    if (!bulk_load_wait(&H.bar, d.wait_tries)) {
+        if (tid == 0) atomicOr(a.flags, LLVQ_FLAG_WAIT_TIMEOUT);
+        return;
+    }
+    // odd warps restate tokens (memory latency) while the even ones decode (instruction issue)
+    if (OUT == kDqWeights && (warp & 1)) dq_stage<GROUPED>(a, H);
 
     bool bad = false;
     int oh = 0, ot = 0, eh = 0, et = 0;       // ring heads and tails (warp-uniform)
@@ -422,7 +426,8 @@ __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typen
     if (threadIdx.x == 0) H.stage_next = 0;
     load_smem_image(&S, d.image, sizeof(typename D::Smem));
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const DqRun run = dq_begin<OUT, GROUPED>(a, H);
+    const DqRun run = dq_groups<OUT, GROUPED>(a, H);
+    dq_begin<OUT, GROUPED>(a, H, run);
     __syncthreads();
     if (OUT == kDqWeights) dq_stage<GROUPED>(a, H);
     bool bad = false;

@@ -35,7 +35,7 @@ struct LpShared {
     unsigned long long full[kLpStages], empty[kLpStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort, nact, pad;
-    int whole, split, units, pad2;
+    int whole, split, units, cap;
     int id[kLinExperts], lo[kLinExperts], hi[kLinExperts], first[kLinExperts + 1];
 };
 __host__ __device__ constexpr size_t lp_smem(bool grouped) {
@@ -170,7 +170,7 @@ __device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u
     }
     x.group = g;
     const int rt = (a.lin.rows + kLinRows - 1) / kLinRows;
-    const int tt = (hi - lo + kLinTokens - 1) / kLinTokens;
+    const int tt = (hi - lo + H.cap - 1) / H.cap;
     const int n = ((hi - lo + tt - 1) / tt + 31) & ~31;
     const int band = local / (kLpBand * tt), in_band = local - band * kLpBand * tt;
     const int width = min(kLpBand, rt - band * kLpBand);
@@ -184,12 +184,47 @@ __device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u
     return x;
 }
 
-// Whole tiles in rounds of all pairs, then the rest, split along K while pairs would idle.
-__device__ __forceinline__ void lp_schedule(LpShared &H, int tiles, int pairs, int nk) {
+// The time of a call's tiles of at most `cap` tokens, in ns, and how many ways its last tiles are split.
+// Measured on 74 pairs: a stage of 64 columns takes 0.33 us with 256 tokens and no less than 0.27 us; the
+// epilogue about 0.7 us per 32 tokens, under the next tile's products but for the last; parts of a split
+// tile about 2.5 us more.  Whole tiles go in rounds of all pairs, the rest is split along K while pairs would idle.
+__device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int &split) {
+    const int stage = max(270, 330 * cap / kLinTokens), ends = 22 * cap;
     const int rest = tiles % pairs;
-    H.whole = tiles - rest;
-    H.split = rest ? max(1, min(pairs / rest, nk / kLpMinSplit)) : 1;
-    H.units = H.whole + rest * H.split;
+    int ns = tiles / pairs * max(nk * stage, ends) + ends;
+    split = 1;
+    if (rest) {
+        const int ways = max(1, min(pairs / rest, nk / kLpMinSplit));
+        const int whole = nk * stage, parts = (nk + ways - 1) / ways * stage + 2500;
+        split = parts < whole ? ways : 1;
+        ns += min(whole, parts);
+    }
+    return ns;
+}
+// The tile size of a call, by one warp: tokens[g] of n groups (in shared memory; or `all` tokens of one).  More
+// and smaller tiles fill idle pairs and shorten the last epilogue, larger ones feed the tensor cores better.
+template <bool GROUPED>
+__device__ __forceinline__ void lp_schedule(LpShared &H, int n, int all, int rt, int pairs, int nk) {
+    const int lane = threadIdx.x & 31, cap = 32 * ((lane & 7) + 1);         // lane i: tiles of 32 (i + 1) tokens
+    int tiles = 0;
+    if (GROUPED) {
+        for (int g = lane >> 3; g < n; g += 4) tiles += (H.hi[g] - H.lo[g] + cap - 1) / cap;
+        tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, 8);
+        tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, 16);
+    } else {
+        tiles = (all + cap - 1) / cap;
+    }
+    tiles *= rt;
+    int split;
+    const int ns = lp_cost(tiles, cap, pairs, nk, split);
+    const unsigned best = __ballot_sync(0xFFFFFFFFu, ns == __reduce_min_sync(0xFFFFFFFFu, ns)) & 0xFFu;
+    if (lane == 31 - __clz(best)) {                           // larger tiles where times are equal
+        H.cap = cap;
+        H.split = split;
+        H.whole = tiles - tiles % pairs;
+        H.units = H.whole + tiles % pairs * split;
+    }
+    __syncwarp();
 }
 
 // What a chunk of 16 columns (tokens t .. t1 - 1 of them) needs from memory besides its accumulators: the
@@ -305,7 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
     const int rt = (a.lin.rows + kLinRows - 1) / kLinRows;
     if (warp == 0) {
         if (lane < 5) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.w : &maps.x[lane - 1]) : "memory");
-        if (!GROUPED && lane == 0) lp_schedule(H, rt * (int)((a.lin.tokens + kLinTokens - 1) / kLinTokens), pairs, nk);
+        if (!GROUPED) lp_schedule<false>(H, 1, (int)a.lin.tokens, rt, pairs, nk);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -317,10 +352,12 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
         if (warp == 0) {
             const int n = max(lin_groups<true>(a.lin, kLinExperts, H.id, H.lo, H.hi), 0);
             __syncwarp();
+            lp_schedule<true>(H, n, 0, rt, pairs, nk);
+            const int cap = H.cap;
             int tiles = 0;
             for (int g0 = 0; g0 < n; g0 += 32) {              // tiles before each group
                 const int g = g0 + lane;
-                const int mine = g < n ? rt * ((H.hi[g] - H.lo[g] + kLinTokens - 1) / kLinTokens) : 0;
+                const int mine = g < n ? rt * ((H.hi[g] - H.lo[g] + cap - 1) / cap) : 0;
                 int sum = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -330,10 +367,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                 if (g < n) H.first[g] = tiles + sum - mine;
                 tiles += __shfl_sync(0xFFFFFFFFu, sum, 31);
             }
-            if (lane == 0) {
-                H.nact = n;
-                lp_schedule(H, tiles, pairs, nk);
-            }
+            if (lane == 0) H.nact = n;
         }
         __syncthreads();
     }
