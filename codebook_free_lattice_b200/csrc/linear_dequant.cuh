@@ -20,14 +20,16 @@ namespace llvq {
 constexpr int kDqThreads = 1024;
 constexpr int kDqWarps = kDqThreads / 32;
 constexpr int kDqRing = 64;                   // records per ring (a warp drains a ring at 32)
+constexpr int kDqRare = 64;                   // records of rare classes kept to the end
 constexpr int kDqAhead = 64;                  // slices between the words read and the words prefetched
 using DqRec = uint4;                          // like BinRec: x, y, z the digits, w = local row | block << 16
 
 struct DqShared {
-    int slice_next, stage_next, nact, pad;
+    int slice_next, stage_next, nact, nrare;
     unsigned long long bar;
     unsigned long long pad2;
     int left[2][32], head[2][32];             // what the rings hold at the end, and where
+    uint4 rare[kDqRare];                      // blocks of the rare classes, decoded at the end
     int id[kLinExperts];                      // the active experts (weights), or DqDots in this place (dots)
 };
 // Few tokens: the activations as fp16, one row of nb * 24 values per token (zero beyond the columns), follow.
@@ -37,7 +39,7 @@ struct DqDots {
     float scale[kLinDots];
 };
 enum DqOut { kDqWeights = 0, kDqDots = 1 };
-constexpr size_t kDqHead = 32 + 4 * 32 * sizeof(int);              // DqShared without its list
+constexpr size_t kDqHead = 32 + 4 * 32 * sizeof(int) + kDqRare * sizeof(uint4);              // DqShared without its list
 __host__ __device__ constexpr size_t dq_tail(int out, bool grouped, long long tokens, int nb) {
     return kDqHead + (out == kDqDots ? sizeof(DqDots) + (size_t)tokens * nb * 48 : grouped ? sizeof(int) * kLinExperts : 0);
 }
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
     if (tid == 0) {
         H.slice_next = kDqWarps;              // slices 0..31 go to warps 0..31 directly
         H.stage_next = 0;
+        H.nrare = 0;
     }
     {
         void *const dst[1] = {&S};
@@ -368,7 +371,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
             rec.x = __ldg(d.tabC + (S.c_offs[cl.cls] & 0x7FFFFu) + pC);
             rec.y = (uint32_t)cl.cls | cl.r << 9 | pS << 21;
         }
-        if (kind == 2) dq48_consume<2, OUT, GAIN, GROUPED>(a, S, H, rec, run.row0);
+        // Odd classes of five magnitude groups and even ones off the tables, 0.12% of the points: a warp that
+        // decoded one where it is met would spend 1500 instructions on one lane, 7% of the kernel's
+        // time, so they wait for the end (as long as there is room)
+        if (kind == 2) {
+            const int at = atomicAdd(&H.nrare, 1);
+            if (at < kDqRare) H.rare[at] = rec;
+            else dq48_consume<2, OUT, GAIN, GROUPED>(a, S, H, rec, run.row0);
+        }
         if (valid && !cl.ok) {                // an index beyond the coded points: nothing
             bad = true;
             long long src, dst;
@@ -410,6 +420,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
                 else dq48_consume<1, OUT, GAIN, GROUPED>(a, S, H, rec, run.row0);
             }
         }
+    }
+    // the rare blocks, by warps that are the last to get a batch of the pool
+    if (warp >= kDqWarps / 2 && warp < kDqWarps / 2 + kDqRare / 32) {
+        const int i = 32 * (warp - kDqWarps / 2) + lane;
+        if (i < min(H.nrare, kDqRare)) dq48_consume<2, OUT, GAIN, GROUPED>(a, S, H, H.rare[i], run.row0);
     }
     if (OUT == kDqWeights) dq_stage<GROUPED>(a, H);
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.flags, LLVQ_FLAG_INDEX_RANGE);
