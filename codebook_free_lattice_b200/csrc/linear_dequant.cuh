@@ -501,10 +501,30 @@ __global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a
     }
     for (int o = blockIdx.x * kDqFinishWarps + warp; o < outs; o += gridDim.x * kDqFinishWarps) {
         const float *row = a.dots + ((long long)t * a.held + (long long)e * a.rows + (GATED ? 2 * o : o)) * a.nb;
+        // bias and residual are on their way while the row is added
+        float zb = 0.f, ub = 0.f, res = 0.f;
+        if (lane == 0) {
+            if (q.bias) {
+                const T *b = static_cast<const T *>(q.bias) + (long long)expert * a.rows + o;
+                zb = lin_load(b);
+                if (GATED) ub = lin_load(b + a.half);
+            }
+            if (q.residual) res = lin_load(static_cast<const T *>(q.residual) + t * q.ld_res + o);
+        }
         float z = 0.f, up = 0.f;
-        for (int j = lane; j < a.nb; j += 32) {
-            z += __ldcg(row + j);
-            if (GATED) up += __ldcg(row + a.nb + j);
+        for (int j0 = 0; j0 < a.nb; j0 += 128) {
+            float v[4], u[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int j = j0 + 32 * i + lane;
+                v[i] = j < a.nb ? __ldcg(row + j) : 0.f;
+                if (GATED) u[i] = j < a.nb ? __ldcg(row + a.nb + j) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                z += v[i];
+                if (GATED) up += u[i];
+            }
         }
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) {
@@ -512,14 +532,11 @@ __global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a
             if (GATED) up += __shfl_xor_sync(0xFFFFFFFFu, up, s);
         }
         if (lane == 0) {
-            if (q.bias) {
-                const T *b = static_cast<const T *>(q.bias) + (long long)expert * a.rows + o;
-                z += lin_load(b);
-                if (GATED) up += lin_load(b + a.half);
-            }
+            z += zb;
+            up += ub;
             float y = q.act == kActNone ? z : lin_activate1(z, q.act);
             if (GATED) y *= up;
-            if (q.residual) y += lin_load(static_cast<const T *>(q.residual) + t * q.ld_res + o);
+            if (q.residual) y += res;
             static_cast<T *>(q.Y)[t * q.ldy + o] = lin_round<T>(y);
         }
     }
