@@ -13,6 +13,10 @@ using namespace llvq;
 namespace {
 
 constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
+// Activations of this many values are restated by a kernel of their own, fewer beside the decode, where a warp takes
+// a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096 over 4096 x 4096 133 against 137, 512 over
+// 1024 x 1024 26 against 19 (one more launch).
+constexpr long long kStageValues = 1 << 21;
 constexpr long long kMaxRunRows = 0xFFFF;                  // row field of a record
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -276,7 +280,15 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;
     for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.cols, pitch, 128 >> b);
     if (!ok) return refuse("sizes or strides beyond a tensor map", LLVQ_ERR_UNSUPPORTED);
-    cudaError_t e = grouped ? launch_dequant<kDqWeights, true>(c, w, l, s) : launch_dequant<kDqWeights, false>(c, w, l, s);
+    cudaError_t e = cudaSuccess;
+    LinArgs first = l;
+    if (l.stage && q->tokens * l.cols >= kStageValues) {
+        const dim3 grid((unsigned)std::min<long long>(q->tokens, (long long)c->num_sms * 32));
+        const int threads = std::min(kLinStageMost, (l.cols + 1023) / 1024 * 32);
+        e = bf16 ? launch(k_linear_stage<true>, grid, threads, 0, s, l) : launch(k_linear_stage<false>, grid, threads, 0, s, l);
+        first.stage = 0;
+    }
+    if (e == cudaSuccess) e = grouped ? launch_dequant<kDqWeights, true>(c, w, first, s) : launch_dequant<kDqWeights, false>(c, w, first, s);
     if (e == cudaSuccess)
         e = grouped ? product_dispatch<true>(c, m, a, q->gated, bf16, s) : product_dispatch<false>(c, m, a, q->gated, bf16, s);
     if (e == cudaSuccess) return LLVQ_OK;

@@ -204,6 +204,61 @@ __device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, in
     for (int i = lane; i < n8; i += 32) dst[i] = lin_restate8(lin_load8(src, 8 * i, cols, wide), f);
 }
 
+// Many tokens restated by a kernel of their own, one CTA per token, the row held in registers between the scale
+// and the conversion (the part of a row beyond 64 values per thread is read again): the bytes of x once in and
+// once out.
+constexpr int kLinStageMost = 1024;           // threads: a row's 16-byte units over 4, in whole warps
+template <bool BF16>
+__global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a) {
+    constexpr int kHeld = 8;
+    __shared__ uint32_t tops[2][kLinStageMost / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, threads = blockDim.x;
+    long long lo = 0, hi = a.tokens;
+    if (a.offsets) {                          // rows that no group has are not read; bad offsets are the decode's to tell
+        lo = max(0, __ldg(a.offsets));
+        hi = min(a.tokens, (long long)__ldg(a.offsets + a.experts));
+    }
+    const int n8 = (a.cols + 7) / 8;
+    int turn = 0;
+    for (long long t = lo + blockIdx.x; t < hi; t += gridDim.x, turn ^= 1) {
+        const uint16_t *src = static_cast<const uint16_t *>(a.X) + t * a.ldx;
+        uint4 *dst = reinterpret_cast<uint4 *>(a.Xs + t * a.ldxs);
+        const bool wide = ((unsigned long long)src & 15ull) == 0ull;
+        uint4 held[kHeld];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; i++) {
+            const int k = tid + threads * i;
+            if (k < n8) held[i] = lin_load8(src, 8 * k, a.cols, wide);
+        }
+        float f = 1.f;
+        if (BF16) {
+#pragma unroll
+            for (int i = 0; i < kHeld; i++)
+                if (tid + threads * i < n8) top = max(top, lin_top8(held[i]));
+            for (int k = tid + threads * kHeld; k < n8; k += threads) top = max(top, lin_top8(lin_load8(src, 8 * k, a.cols, wide)));
+            top = warp_max(top);
+            if ((tid & 31) == 0) tops[turn][tid >> 5] = top;
+            __syncthreads();
+            top = warp_max((tid & 31) < threads >> 5 ? tops[turn][tid & 31] : 0u);
+            const float inv = lin_token_scale(top);
+            if (tid == 0) a.token_scale[t] = inv;
+            f = pow2_inverse(inv);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; i++) {
+            const int k = tid + threads * i;
+            if (k < n8) dst[k] = BF16 ? lin_restate8(held[i], f) : held[i];
+        }
+        for (int k = tid + threads * kHeld; k < n8; k += threads) {
+            const uint4 q = lin_load8(src, 8 * k, a.cols, wide);
+            dst[k] = BF16 ? lin_restate8(q, f) : q;
+        }
+    }
+}
+
 // Activations, four values at a time and out of line: the code of one activation is fetched once, and
 // a kernel that needs none of it does not step over it.  Each is written so that its negative tail keeps
 // its accuracy: z / (1 + e^-u), and for gelu the complementary error function by the rational

@@ -296,6 +296,34 @@ def test_strides_and_addresses(codecs, tokens, dtype):
         assert torch.equal(out[:, :3], kept[:, :3]) and torch.equal(out[:, 93:], kept[:, 93:])
 
 
+@pytest.mark.parametrize("tokens,cols,dtype,grouped", [
+    (2100, 1001, "bfloat16", False), (2200, 1000, "bfloat16", True), (2200, 999, "float16", False), (70, 33000, "bfloat16", False)])
+def test_many_values_restated(codecs, tokens, cols, dtype, grouped):
+    """Enough activations for the kernel that restates them by itself; rows beyond what its threads hold, too."""
+    dtype = getattr(torch, dtype)
+    layer = Layer(codecs, 48, 48, cols, seed=7)
+    x = tokens_of(3, tokens, cols, dtype)
+    x = (x.double() * torch.tensor([1.0, 2.0 ** -60 if dtype is torch.bfloat16 else 2.0 ** -6], device="cuda", dtype=torch.float64)
+         [torch.arange(tokens, device="cuda") % 2, None]).to(dtype)
+    if grouped:
+        x[:30], x[-40:] = float("nan"), float("inf")
+        edges = [30, 700, 700, tokens - 40]
+        y = random(1, (tokens, 16), dtype)
+        kept = y.clone()
+        layer.codec.linear_grouped(layer.weight, 3, x, torch.tensor(edges, dtype=torch.int32, device="cuda"), y)
+        parts = [expected(layer.dense[16 * e:16 * e + 16], x[edges[e]:edges[e + 1]]) for e in (0, 2)]
+        want = [torch.cat(t) for t in zip(*parts)]
+        assert torch.equal(y[:30], kept[:30]) and torch.equal(y[-40:], kept[-40:])
+        y = y[30:-40]
+    else:
+        y = torch.empty(tokens, 48, dtype=dtype, device="cuda")
+        layer.codec.linear(layer.weight, x, y)
+        want = expected(layer.dense, x)
+    for k in range(2):
+        check(y[k::2].contiguous(), *(t[k::2] for t in want))
+    assert layer.codec.get_error() == 0
+
+
 @pytest.mark.parametrize("tokens", (1, 64, 400))
 @pytest.mark.parametrize("gated", (False, True))
 def test_residual_in_place_and_broadcast(codecs, tokens, gated):
