@@ -17,6 +17,9 @@ constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a 
 // a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096 over 4096 x 4096 133 against 137, 512 over
 // 1024 x 1024 26 against 19 (one more launch).
 constexpr long long kStageValues = 1 << 21;
+// A wait of the product covers a whole tile (milliseconds for the longest rows), not one round of few products:
+// 16 times the polls
+constexpr uint32_t kWaitRounds = 16;
 constexpr long long kMaxRunRows = 0xFFFF;                  // row field of a record
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -42,6 +45,7 @@ struct Plan {
     int stage = 0;                                         // LinArgs::stage
     long long held = 0;                                    // rows of the decoded weight
     long long w_pitch = 0, xs_pitch = 0;
+    bool far = false;                                      // ... with the activations in the workspace
     bool dots = false;                                     // few tokens: no decoded weight
     size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
 };
@@ -63,10 +67,18 @@ int dequant_ctas(int bits) { return bits == 48 ? 1 : bits == 72 ? Dec72::kCtasPe
 // and 48 written bytes per block once: on one matrix of 4096 x 4096, 1 / 2 / 3 / 4 tokens take 29.6 / 32.7 / 35.5 /
 // 38.7 us against 39.2, on 22016 x 4096 three 141 against 148 and four 159.  Over experts what counts is how many
 // tokens one gets: at most one on average (8 tokens, 8 experts of 2816 x 2048: 55 us against 58; over 4 experts 44
-// against 42).  The activations have to fit in shared memory beside the decoder's tables.
-bool few_tokens(const llvq_codec *c, const llvq_weight *w, int64_t tokens, int experts, bool grouped) {
-    return tokens <= std::max(3, std::min(experts, kLinDots)) &&
-           dequant_smem(c->index_bits, kDqDots, grouped, tokens, w->blocks_per_row) <= kSmemLimit / dequant_ctas(c->index_bits) - 1024;
+// against 42).
+//
+// Activations that do not fit in shared memory beside the decoder's tables are restated in the workspace and read
+// through L1: dearer per token, so two tokens of one matrix rather than three (4096 x 11008: 70.8 us against
+// 74.3, three 82.9; one token of 8192 x 28672 287 us against 340; 8 tokens over 64 experts of 1408 x 7168 111
+// against 132).
+enum Few { kManyTokens, kFewNear, kFewFar };
+Few few_tokens(int bits, bool grouped, int64_t tokens, int experts, int nb) {
+    const int shared = std::min(experts, kLinDots);
+    if (tokens > std::max(3, shared)) return kManyTokens;
+    if (dequant_smem(bits, kDqDots, grouped, tokens, nb) <= kSmemLimit / dequant_ctas(bits) - 1024) return kFewNear;
+    return tokens <= std::max(2, shared) ? kFewFar : kManyTokens;
 }
 
 // Checks a call (everything but the workspace) and lays out its workspace.
@@ -76,7 +88,7 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
     const llvq_status st = check_weight(c, w);
     if (st != LLVQ_OK) return refuse("weight: null or misaligned pointer, size, pitch or budget mismatch");
     if (w->cols < 1) return refuse("a linear layer has at least one column");
-    if (q->tokens < 0 || q->tokens > 0x7FFFF000ll) return refuse("tokens out of range");
+    if (q->tokens < 0 || q->tokens > 1ll << 30) return refuse("tokens out of range");
     if (q->dtype != LLVQ_DTYPE_FP16 && q->dtype != LLVQ_DTYPE_BF16) return refuse("dtype is neither fp16 nor bf16");
     if (q->activation < LLVQ_ACT_NONE || q->activation > LLVQ_ACT_SILU) return refuse("unknown activation");
     if (q->gated != 0 && q->gated != 1) return refuse("gated is 0 or 1");
@@ -112,9 +124,16 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         at += round256(bytes);
         return here;
     };
-    p.dots = few_tokens(c, w, q->tokens, p.experts, grouped);
-    if (p.dots) {
+    const Few few = few_tokens(c->index_bits, grouped, q->tokens, p.experts, w->blocks_per_row);
+    if (few != kManyTokens) {
+        p.dots = true;
         p.w = place((size_t)q->tokens * p.held * w->blocks_per_row * sizeof(float));
+        p.far = few == kFewFar;
+        if (p.far) {
+            p.xs_pitch = (long long)w->blocks_per_row * 24;
+            p.xs = place((size_t)q->tokens * p.xs_pitch * sizeof(__half));
+            p.token_scale = place((size_t)q->tokens * sizeof(float));
+        }
         p.bytes = at;
         return LLVQ_OK;
     }
@@ -170,6 +189,12 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cu
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
+cudaError_t launch_stage(const llvq_codec *c, const LinArgs &a, bool bf16, int units, cudaStream_t st) {
+    const dim3 grid((unsigned)std::min<long long>(a.tokens, (long long)c->num_sms * 32));
+    const int threads = std::min(kLinStageMost, (units + 127) / 128 * 32);
+    return launch(bf16 ? k_linear_stage<true> : k_linear_stage<false>, grid, threads, 0, st, a, units);
+}
+
 template <int OUT, bool GROUPED>
 cudaError_t launch_dequant(const llvq_codec *c, const llvq_weight *w, const LinArgs &a, cudaStream_t st) {
     const size_t smem = dequant_smem(c->index_bits, OUT, GROUPED, a.tokens, a.nb);
@@ -222,6 +247,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     if (st != LLVQ_OK) return st;
     if (q->tokens == 0 || p.rows == 0) return LLVQ_OK;
     if (!q->x || !q->y) return refuse("null x or y");
+    if (q->x == q->y) return refuse("y is x: other outputs still need what would be overwritten");
     if (grouped != (q->offsets != nullptr)) return refuse(grouped ? "null offsets" : "offsets without groups");
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes) return refuse("workspace null, misaligned or too small");
     DeviceScope scope(c->device);
@@ -260,7 +286,10 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     const bool bf16 = l.bf16;
     if (p.dots) {
         const DqEnds ends{q->bias, q->residual, q->residual_stride, q->y, q->y_stride, q->activation};
-        cudaError_t e = grouped ? launch_dequant<kDqDots, true>(c, w, l, s) : launch_dequant<kDqDots, false>(c, w, l, s);
+        cudaError_t e = p.far ? launch_stage(c, l, bf16, 3 * l.nb, s) : cudaSuccess;
+        if (e == cudaSuccess)
+            e = p.far ? (grouped ? launch_dequant<kDqDotsFar, true>(c, w, l, s) : launch_dequant<kDqDotsFar, false>(c, w, l, s))
+                      : (grouped ? launch_dequant<kDqDots, true>(c, w, l, s) : launch_dequant<kDqDots, false>(c, w, l, s));
         if (e == cudaSuccess) e = grouped ? finish_dispatch<true>(l, ends, q->gated, bf16, s) : finish_dispatch<false>(l, ends, q->gated, bf16, s);
         return e == cudaSuccess ? LLVQ_OK : refuse(cudaGetErrorString(e), LLVQ_ERR_CUDA);
     }
@@ -272,7 +301,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     a.ldy = q->y_stride;
     a.act = q->activation;
     a.partial = (float *)(ws + p.partial);
-    a.wait_tries = g_mma_wait_tries.load();
+    a.wait_tries = std::min(g_mma_wait_tries.load(), 1u << 27) * kWaitRounds;
     LpMaps m;
     bool ok = make_map(m.w, l.W, p.held, l.cols, l.ldw, 128);
     const void *x = p.stage ? (const void *)l.Xs : q->x;
@@ -283,9 +312,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     cudaError_t e = cudaSuccess;
     LinArgs first = l;
     if (l.stage && q->tokens * l.cols >= kStageValues) {
-        const dim3 grid((unsigned)std::min<long long>(q->tokens, (long long)c->num_sms * 32));
-        const int threads = std::min(kLinStageMost, (l.cols + 1023) / 1024 * 32);
-        e = bf16 ? launch(k_linear_stage<true>, grid, threads, 0, s, l) : launch(k_linear_stage<false>, grid, threads, 0, s, l);
+        e = launch_stage(c, l, bf16, (l.cols + 7) / 8, s);
         first.stage = 0;
     }
     if (e == cudaSuccess) e = grouped ? launch_dequant<kDqWeights, true>(c, w, first, s) : launch_dequant<kDqWeights, false>(c, w, first, s);
@@ -305,6 +332,10 @@ void allow_all() {
     allow(k_dequant48<kDqWeights, 1, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDots, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDots, 1, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqDotsFar, 0, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqDotsFar, 1, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec72, kDqDotsFar, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec96, kDqDotsFar, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec72, kDqWeights, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec72, kDqDots, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec96, kDqWeights, GROUPED>, kSmemLimit);
@@ -332,6 +363,7 @@ void llvq::set_linear_attrs(llvq_codec *c) {
         n = c->num_sms / 2;
     }
     c->pairs = std::max(1, std::min(n, c->num_sms / 2));
+    encode_tiled();                                        // looked up here, not inside a stream capture
 }
 
 extern "C" {

@@ -206,10 +206,10 @@ __device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, in
 
 // Many tokens restated by a kernel of their own, one CTA per token, the row held in registers between the scale
 // and the conversion (the part of a row beyond 64 values per thread is read again): the bytes of x once in and
-// once out.
+// once out.  units: 16-byte units of a row to write, zero beyond the columns.
 constexpr int kLinStageMost = 1024;           // threads: a row's 16-byte units over 4, in whole warps
 template <bool BF16>
-__global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a) {
+__global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int units) {
     constexpr int kHeld = 8;
     __shared__ uint32_t tops[2][kLinStageMost / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a) {
         lo = max(0, __ldg(a.offsets));
         hi = min(a.tokens, (long long)__ldg(a.offsets + a.experts));
     }
-    const int n8 = (a.cols + 7) / 8;
+    const int n8 = units;
     int turn = 0;
     for (long long t = lo + blockIdx.x; t < hi; t += gridDim.x, turn ^= 1) {
         const uint16_t *src = static_cast<const uint16_t *>(a.X) + t * a.ldx;

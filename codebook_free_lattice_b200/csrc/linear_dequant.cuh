@@ -32,16 +32,18 @@ struct DqShared {
     uint4 rare[kDqRare];                      // blocks of the rare classes, decoded at the end
     int id[kLinExperts];                      // the active experts (weights), or DqDots in this place (dots)
 };
-// Few tokens: the activations as fp16, one row of nb * 24 values per token (zero beyond the columns), follow.
+// Few tokens: the activations as fp16, one row of nb * 24 values per token (zero beyond the columns), follow, or are
+// in the workspace where they do not fit (kDqDotsFar: restated by k_linear_stage, read through L1).
 struct DqDots {
     int id[kLinDots], lo[kLinDots], hi[kLinDots];
     uint32_t top[kLinDots];
     float scale[kLinDots];
 };
-enum DqOut { kDqWeights = 0, kDqDots = 1 };
+enum DqOut { kDqWeights = 0, kDqDots = 1, kDqDotsFar = 2 };
 constexpr size_t kDqHead = 32 + 4 * 32 * sizeof(int) + kDqRare * sizeof(uint4);              // DqShared without its list
 __host__ __device__ constexpr size_t dq_tail(int out, bool grouped, long long tokens, int nb) {
-    return kDqHead + (out == kDqDots ? sizeof(DqDots) + (size_t)tokens * nb * 48 : grouped ? sizeof(int) * kLinExperts : 0);
+    return kDqHead + (out == kDqDots ? sizeof(DqDots) + (size_t)tokens * nb * 48
+                      : out == kDqDotsFar ? sizeof(DqDots) : grouped ? sizeof(int) * kLinExperts : 0);
 }
 __host__ __device__ constexpr size_t dq48_fixed() { return sizeof(SmemGv48) + sizeof(DqRec) * (kDqWarps * 2 * kDqRing); }
 template <class D>
@@ -107,16 +109,17 @@ __device__ __forceinline__ void dq_store_zero(__half *out) {
     p[0] = p[1] = p[2] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// A block's dot products with the tokens of its expert, from shared memory: 24 exact products each, fp32 sums.
+// A block's dot products with the tokens of its expert: 24 exact products each, fp32 sums.
+template <int OUT>
 __device__ __forceinline__ void dq_dots(const LinArgs &a, const DqDots &D, const uint32_t wh[12], float scale, int t0, int t1,
                                         long long row, int j) {
     const uint4 *x = reinterpret_cast<const uint4 *>(&D + 1) + 3 * j;
     for (int t = t0; t < t1; t++) {
-        const uint4 *xt = x + 3 * t * a.nb;
+        const uint4 *xt = OUT == kDqDots ? x + 3 * t * a.nb : reinterpret_cast<const uint4 *>(a.Xs + t * a.ldxs) + 3 * j;
         float d0 = 0.f, d1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 3; c++) {
-            const uint4 q = xt[c];
+            const uint4 q = OUT == kDqDots ? xt[c] : __ldg(xt + c);
             d0 = fma2_f16_f32(wh[4 * c + 0], q.x, d0);
             d1 = fma2_f16_f32(wh[4 * c + 1], q.y, d1);
             d0 = fma2_f16_f32(wh[4 * c + 2], q.z, d0);
@@ -135,7 +138,7 @@ __device__ __forceinline__ void dq_block(const LinArgs &a, const DqShared &H, co
     } else {
         const DqDots &D = *reinterpret_cast<const DqDots *>(H.id);
         const int e = GROUPED ? (int)div_by((uint32_t)active, (uint32_t)a.rows, a.rows_recip) : 0;
-        dq_dots(a, D, wh, scale, GROUPED ? D.lo[e] : 0, GROUPED ? D.hi[e] : (int)a.tokens, dst, j);
+        dq_dots<OUT>(a, D, wh, scale, GROUPED ? D.lo[e] : 0, GROUPED ? D.hi[e] : (int)a.tokens, dst, j);
     }
 }
 // ... and of a block whose index is not coded
@@ -193,7 +196,7 @@ __device__ __forceinline__ DqRun dq_groups(const LinArgs &a, DqShared &H) {
     if (GROUPED) {
         if (warp == 0) {
             DqDots &D = *reinterpret_cast<DqDots *>(H.id);
-            const int n = OUT == kDqDots ? lin_groups<true>(a, kLinDots, D.id, D.lo, D.hi)
+            const int n = OUT != kDqWeights ? lin_groups<true>(a, kLinDots, D.id, D.lo, D.hi)
                                          : lin_groups<false>(a, kLinExperts, H.id, nullptr, nullptr);
             if (lane == 0) H.nact = max(n, 0);
             if (n < 0 && lane == 0 && blockIdx.x == 0) atomicOr(a.flags, LLVQ_FLAG_OFFSETS);
@@ -208,6 +211,10 @@ __device__ __forceinline__ void dq_begin(const LinArgs &a, DqShared &H, const Dq
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     if constexpr (OUT == kDqDots) {
         dq_stage_dots(a, *reinterpret_cast<DqDots *>(H.id));
+        return;
+    }
+    if constexpr (OUT == kDqDotsFar) {
+        if (threadIdx.x < a.tokens) reinterpret_cast<DqDots *>(H.id)->scale[threadIdx.x] = a.bf16 ? __ldg(a.token_scale + threadIdx.x) : 1.f;
         return;
     }
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x) a.counters[i] = 0u;

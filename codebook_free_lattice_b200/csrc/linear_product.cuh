@@ -191,7 +191,7 @@ __device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u
 __device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int &split) {
     const int stage = max(270, 330 * cap / kLinTokens), ends = 22 * cap;
     const int rest = tiles % pairs;
-    int ns = tiles / pairs * max(nk * stage, ends) + ends;
+    long long ns = (long long)(tiles / pairs) * max(nk * stage, ends) + ends;
     split = 1;
     if (rest) {
         const int ways = max(1, min(pairs / rest, nk / kLpMinSplit));
@@ -199,7 +199,7 @@ __device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, in
         split = parts < whole ? ways : 1;
         ns += min(whole, parts);
     }
-    return ns;
+    return (int)min(ns, 0x7FFFFFFFll);
 }
 // The tile size of a call, by one warp: tokens[g] of n groups (in shared memory; or `all` tokens of one).  More
 // and smaller tiles fill idle pairs and shorten the last epilogue, larger ones feed the tensor cores better.

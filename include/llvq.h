@@ -272,7 +272,7 @@ llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int3
  * used.  An expert without tokens costs nothing: its blocks are not decoded.  Offsets that fall or leave
  * 0 .. tokens raise LLVQ_FLAG_OFFSETS, and then nothing of y is written. */
 typedef struct {
-    int64_t tokens;            /* rows of x, residual and y (the room, for grouped calls) */
+    int64_t tokens;            /* rows of x, residual and y (the room, for grouped calls), at most 2^30 */
     int32_t dtype;             /* LLVQ_DTYPE_* */
     int32_t activation;        /* LLVQ_ACT_* */
     int32_t gated;             /* 0 or 1 */

@@ -158,6 +158,9 @@ CASES = [
     (1, 300, 1000, "float16", "none", False, False, True, "table"),
     (1, 300, 1000, "bfloat16", "gelu", False, True, True, "direct"),
     (2, 130, 2005, "float16", "silu", True, True, True, "table"),
+    (1, 50, 24001, "bfloat16", "silu", True, True, True, "table"),
+    (2, 33, 30000, "float16", "none", False, False, True, "direct"),
+    (3, 20, 30000, "bfloat16", "none", False, True, False, "table"),
     (3, 513, 25, "float16", "relu", False, True, False, "direct"),
     (5, 64, 23, "bfloat16", "gelu_tanh", False, False, True, "table"),
     (16, 256, 1024, "float16", "gelu_tanh", False, True, True, "table"),
@@ -209,6 +212,8 @@ GROUPED = [
     (1, 7, 64, 48, "bfloat16", "silu", True, True, True, "table", "one", 0, 3),
     (9, 40, 130, 333, "float16", "gelu", False, True, True, "table", "each", 2, 1),
     (16, 64, 96, 512, "bfloat16", "silu", True, False, False, "table", "uneven", 0, 0),
+    (16, 20, 34, 2500, "float16", "silu", True, True, True, "table", "uneven", 0, 0),
+    (5, 12, 20, 9001, "bfloat16", "gelu", False, False, False, "direct", "uneven", 4, 7),
     (77, 5, 331, 1000, "float16", "gelu", False, True, True, "direct", "ends", 0, 19),
     (300, 3, 258, 200, "bfloat16", "relu", False, False, True, "table", "one", 5, 0),
     (700, 9, 514, 130, "float16", "gelu_tanh", True, True, True, "table", "uneven", 1, 40),

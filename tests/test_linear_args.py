@@ -60,7 +60,7 @@ def weight(L, rows=64, cols=100, bits=48, **other):
 
 
 def call(L, tokens=5, rows=64, cols=100, **other):
-    q = L.llvq_linear_call(tokens, L.LLVQ_DTYPE_FP16, L.LLVQ_ACT_NONE, 0, 0, ADDRESS, cols, None, None, 0, ADDRESS, rows, None)
+    q = L.llvq_linear_call(tokens, L.LLVQ_DTYPE_FP16, L.LLVQ_ACT_NONE, 0, 0, ADDRESS, cols, None, None, 0, 2 * ADDRESS, rows, None)
     for k, v in other.items():
         setattr(q, k, v)
     return q
@@ -71,6 +71,7 @@ REFUSED = [
     (dict(experts=2), {}), (dict(x_stride=99), {}), (dict(y_stride=63), {}), (dict(residual=ADDRESS, residual_stride=63), {}),
     (dict(residual=ADDRESS, residual_stride=-64), {}), (dict(x=ADDRESS + 1), {}), (dict(y=ADDRESS + 1), {}),
     (dict(bias=ADDRESS + 1), {}), (dict(residual=ADDRESS + 1), {}), (dict(x=None), {}), (dict(y=None), {}),
+    (dict(y=ADDRESS), {}), (dict(tokens=(1 << 30) + 1), {}),
     (dict(offsets=ADDRESS), {}), ({}, dict(cols=0, blocks_per_row=0)), ({}, dict(rows=-1)), ({}, dict(words=None)),
     ({}, dict(index_bits=72)), ({}, dict(row_pitch_words=4)), ({}, dict(gains=ADDRESS + 1)), ({}, dict(words=ADDRESS + 4)),
     (dict(gated=1), dict(rows=63)),
@@ -155,6 +156,9 @@ def test_workspace_sizes(L, bare, bits):
     assert need(1000, 1000, 64, dtype=1) == base(1000, 1000) + 64 * 1024 * 2 + 256
     assert need(4096, 4096, 3) == 3 * 4096 * 171 * 4
     assert need(4096, 4096, 1, dtype=1) == 4096 * 171 * 4
+    if bits == 48:                                     # ... and what does not fit in shared memory, restated
+        assert need(64, 28672, 2) == up256(2 * 64 * 1195 * 4) + up256(2 * 1195 * 48) + 256
+        assert need(64, 28672, 3) == base(64, 28672)
     # experts: as many as can have a token are decoded
     assert need(64 * 100, 8192, 20, experts=64) == base(20 * 100, 8192)
     assert need(64 * 100, 8192, 1000, experts=64) == base(64 * 100, 8192)
