@@ -7,7 +7,7 @@
 // per thread and the number of tokens, which varies, is the N side in steps of 32.  Each CTA loads its
 // 128 weight rows and its half of the tokens (TMA, 128-byte swizzle, 64 columns of K per stage); fp32
 // accumulators sit in both CTAs' TMEM, two sets of 256 columns, so that one tile's epilogue runs under
-// the next tile's products.  Warp 0 loads, warp 1 of the leading CTA issues the products, warps 2 to 9
+// the next tile's products.  Warp 0 loads, warp 1 of the leading CTA issues the products, warps 2 to 17
 // run the epilogue.
 //
 // A persistent grid walks the tiles of all groups.  Tiles that do not fill a last round of pairs are
@@ -20,8 +20,9 @@
 
 namespace llvq {
 
-constexpr int kLpThreads = 320;
-constexpr int kLpEpilogueWarps = 8;
+constexpr int kLpEpilogueWarps = 16;                       // four per quarter of the TMEM lanes
+constexpr int kLpEach = kLpEpilogueWarps / 4;              // a warp takes every fourth chunk of 16 columns
+constexpr int kLpThreads = 32 * (2 + kLpEpilogueWarps);
 constexpr int kLpStages = 6;
 constexpr int kLpK = 64;                                   // columns of K per stage: one 128-byte swizzle row
 constexpr int kLpABytes = 128 * kLpK * 2;                  // 128 weight rows
@@ -86,19 +87,6 @@ __device__ __forceinline__ bool lp_wait(uint32_t bar, uint32_t parity, uint32_t 
     for (uint32_t i = 0; i < tries; i++)
         if (mbar_try_wait_parity(bar, parity)) return true;
     return false;
-}
-// barrier of the epilogue warps; true when every thread says so
-__device__ __forceinline__ bool lp_epilogue_all(bool mine) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"((uint32_t)mine), "r"(kLpEpilogueWarps * 32)
-        : "memory");
-    return all != 0u;
 }
 __device__ __forceinline__ void lp_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -471,8 +459,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
     } else {
-        // ---- epilogue: warp quarter (TMEM lanes) and which of the 32-column chunks
-        const int quarter = warp & 3, odd = (warp - 2) >> 2;
+        // ---- epilogue: warp quarter (TMEM lanes) and which of the chunks
+        const int quarter = warp & 3, part = (warp - 2) >> 2;
         const int lrow = quarter * 32 + lane;                  // row within the CTA's 128
         const uint32_t tlane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t tile = 0;
@@ -489,12 +477,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                     bias = lin_load(static_cast<const T *>(a.bias) + (long long)x.expert * a.lin.rows +
                                     (GATED ? (row >> 1) + (row & 1) * a.lin.half : row));
             }
-            // all epilogue warps go on, or none (they meet at a barrier again when a tile is split)
             ok = lp_wait(smem_u32(&H.acc_full[b]), (tile >> 1) & 1u, tries) && !*abort_flag;
-            ok = lp_epilogue_all(ok);
-            if (!ok) break;
+            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            // this warp's chunks of 16 columns: every other one
+            // this warp's chunks of 16 columns: part, part + kLpEach, ...
             const int chunks = (x.t1 - x.t0 + 15) >> 4;
             const uint32_t acc = tlane + b * kLinTokens;
             uint32_t mine = 0xFFFFFFFFu;                       // chunks to finish here
@@ -503,7 +489,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                 // partial sums to the workspace, four columns of a row together; whichever split of a
                 // chunk arrives last finishes it
                 float4 *own = reinterpret_cast<float4 *>(a.partial) + ((long long)x.slot * 2 + rank) * (kLinTokens * 32) + lrow;
-                for (int c = odd; c < chunks; c += 2) {
+                for (int c = part; c < chunks; c += kLpEach) {
                     float z[16];
                     lp_tmem_load(acc + 16 * c, z);
 #pragma unroll
@@ -513,18 +499,18 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                 __threadfence();
                 __syncwarp();
                 unsigned before = 0;
-                const int c = 2 * lane + odd;
-                if (lane < 8 && c < chunks) before = atomicAdd(a.lin.counters + ((x.tile * 2 + rank) * 4 + quarter) * 16 + c, 1u);
-                mine = __ballot_sync(0xFFFFFFFFu, lane < 8 && before == (unsigned)(x.split - 1));
+                const int c = kLpEach * lane + part;
+                if (lane < 16 / kLpEach && c < chunks) before = atomicAdd(a.lin.counters + ((x.tile * 2 + rank) * 4 + quarter) * 16 + c, 1u);
+                mine = __ballot_sync(0xFFFFFFFFu, lane < 16 / kLpEach && c < chunks && before == (unsigned)(x.split - 1));
                 __threadfence();
                 parts = reinterpret_cast<const float4 *>(a.partial) +
                         ((long long)x.tile * x.split * 2 + rank) * (kLinTokens * 32) + lrow;
             }
-            mine &= (1u << ((chunks - odd + 1) >> 1)) - 1u;
+            mine &= (1u << ((chunks - part + kLpEach - 1) / kLpEach)) - 1u;
             LpEnds<GATED, T> ends;
-            if (mine) lp_load_ends<GATED, T>(a, ends, x.t0 + 16 * (2 * (__ffs(mine) - 1) + odd), x.t1, row, row_in, lane);
+            if (mine) lp_load_ends<GATED, T>(a, ends, x.t0 + 16 * (kLpEach * (__ffs(mine) - 1) + part), x.t1, row, row_in, lane);
             while (mine) {
-                const int c = 2 * (__ffs(mine) - 1) + odd;
+                const int c = kLpEach * (__ffs(mine) - 1) + part;
                 mine &= mine - 1u;
                 float z[16];
                 if (x.split > 1) {
@@ -546,13 +532,13 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                     lp_tmem_load(acc + 16 * c, z);
                 }
                 const LpEnds<GATED, T> now = ends;
-                if (mine) lp_load_ends<GATED, T>(a, ends, x.t0 + 16 * (2 * (__ffs(mine) - 1) + odd), x.t1, row, row_in, lane);
+                if (mine) lp_load_ends<GATED, T>(a, ends, x.t0 + 16 * (kLpEach * (__ffs(mine) - 1) + part), x.t1, row, row_in, lane);
                 lp_outputs<GATED, T>(a, z, now, rs, bias, x.t0 + 16 * c, x.t1, row, row_in, lane);
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];"
                              ::"r"(lp_leader(smem_u32(&H.acc_empty[b]))) : "memory");
         }
         if (!ok && lane == 0) *abort_flag = 1;
