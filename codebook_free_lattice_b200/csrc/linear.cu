@@ -221,8 +221,12 @@ cudaError_t launch_dequant(const llvq_codec *c, const llvq_weight *w, const LinA
 template <bool GROUPED, bool GATED, class T>
 cudaError_t launch_finish(const LinArgs &a, const DqEnds &e, cudaStream_t st) {
     const int outs = GATED ? a.half : a.rows;
-    const int blocks = std::min((outs + kDqFinishWarps - 1) / kDqFinishWarps, 4096);
-    return launch(k_linear_finish<GROUPED, GATED, T>, dim3((unsigned)blocks, (unsigned)a.tokens), 32 * kDqFinishWarps, 0, st, a, e);
+    const int each = kDqFinishWarps * 32 / finish_width(a.nb);             // outputs of a block
+    const int blocks = std::min((outs + each - 1) / each, 4096);
+    auto kernel = finish_width(a.nb) == 32  ? k_linear_finish<GROUPED, GATED, T, 32>
+                  : finish_width(a.nb) == 8 ? k_linear_finish<GROUPED, GATED, T, 8>
+                                            : k_linear_finish<GROUPED, GATED, T, 1>;
+    return launch(kernel, dim3((unsigned)blocks, (unsigned)a.tokens), 32 * kDqFinishWarps, 0, st, a, e);
 }
 template <bool GROUPED>
 cudaError_t finish_dispatch(const LinArgs &a, const DqEnds &e, bool gated, bool bf16, cudaStream_t st) {

@@ -161,7 +161,7 @@ __device__ __forceinline__ void dq_stage_dots(const LinArgs &a, DqDots &D) {
     auto load = [&](int i, int &t) {
         t = i / n8;
         const uint16_t *src = static_cast<const uint16_t *>(a.X) + t * a.ldx;
-        return lin_load8(src, 8 * (i - t * n8), a.cols, ((unsigned long long)src & 15ull) == 0ull);
+        return lin_load8(src, 8 * (i - t * n8), a.cols, lin_wide(src));
     };
     if (!a.bf16) {
         for (int i = threadIdx.x; i < total; i += blockDim.x) {
@@ -221,7 +221,7 @@ __device__ __forceinline__ void dq_begin(const LinArgs &a, DqShared &H, const Dq
     for (int i = warp; i < run.nrows; i += warps) {
         long long src, dst;
         dq_row<GROUPED>(a, H.id, run.row0 + i, src, dst);
-        const float s = lin_row_scale(a, src);
+        const float s = lin_row_scale(a, warp_max(lin_row_top(a, src)));
         if (lane == 0) a.row_scale[dst] = s;       // a row shared with the next CTA gets the same value twice
     }
 }
@@ -243,8 +243,11 @@ __device__ __forceinline__ void dq_stage(const LinArgs &a, DqShared &H) {
         i = __shfl_sync(0xFFFFFFFFu, i, 0);
         const long long t = lo + blockIdx.x + (long long)i * gridDim.x;
         if (t >= hi) break;
-        lin_stage_token(static_cast<const uint16_t *>(a.X) + t * a.ldx, reinterpret_cast<uint4 *>(a.Xs + t * a.ldxs), a.cols,
-                        a.stage == 2 ? a.token_scale + t : nullptr);
+        const uint16_t *src = static_cast<const uint16_t *>(a.X) + t * a.ldx;
+        uint4 *dst = reinterpret_cast<uint4 *>(a.Xs + t * a.ldxs);
+        float *scale = a.stage == 2 ? a.token_scale + t : nullptr;
+        if (!lin_wide(src) && a.cols > kLinShiftedCols) lin_stage_token<true>(src, dst, a.cols, scale);
+        else lin_stage_token<false>(src, dst, a.cols, scale);
     }
 }
 
@@ -473,9 +476,9 @@ __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typen
     if (__any_sync(0xFFFFFFFFu, bad) && (threadIdx.x & 31) == 0) atomicOr(a.flags, LLVQ_FLAG_INDEX_RANGE);
 }
 
-// The second kernel of a call of few tokens: one warp per output adds the dot products of its row (or gate and
-// up rows), lane by lane and then across the lanes, always in the same order, and applies the epilogue.
-// Bound by its latency: 2.8 MB are read for a 4096 x 4104 layer and one token.
+// The second kernel of a call of few tokens: a warp, or 2^k lanes of one for short rows, per output adds the dot
+// products of its row (or gate and up rows), lane by lane and then across the lanes, always in the same order, and
+// applies the epilogue.  Bound by its latency: 2.8 MB are read for a 4096 x 4104 layer and one token.
 struct DqEnds {
     const void *bias, *residual;
     long long ld_res;
@@ -484,7 +487,9 @@ struct DqEnds {
     int act;
 };
 constexpr int kDqFinishWarps = 8;
-template <bool GROUPED, bool GATED, class T>
+// lanes of an output
+__host__ __device__ constexpr int finish_width(int nb) { return nb > 32 ? 32 : nb > 4 ? 8 : 1; }
+template <bool GROUPED, bool GATED, class T, int WIDTH>
 __global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a, DqEnds q) {
     __shared__ int id[kLinDots], lo[kLinDots], hi[kLinDots], count;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -506,11 +511,15 @@ __global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a
         if (e == count || t < lo[e]) return;
         expert = id[e];
     }
-    for (int o = blockIdx.x * kDqFinishWarps + warp; o < outs; o += gridDim.x * kDqFinishWarps) {
+    constexpr int each = 32 / WIDTH;                                       // outputs of a warp
+    const int sub = lane & (WIDTH - 1);
+    for (int o0 = (blockIdx.x * kDqFinishWarps + warp) * each; o0 < outs; o0 += gridDim.x * kDqFinishWarps * each) {
+        const int o = min(o0 + lane / WIDTH, outs - 1);
         const float *row = a.dots + ((long long)t * a.held + (long long)e * a.rows + (GATED ? 2 * o : o)) * a.nb;
         // bias and residual are on their way while the row is added
         float zb = 0.f, ub = 0.f, res = 0.f;
-        if (lane == 0) {
+        const bool writes = sub == 0 && o0 + lane / WIDTH < outs;
+        if (writes) {
             if (q.bias) {
                 const T *b = static_cast<const T *>(q.bias) + (long long)expert * a.rows + o;
                 zb = lin_load(b);
@@ -519,11 +528,11 @@ __global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a
             if (q.residual) res = lin_load(static_cast<const T *>(q.residual) + t * q.ld_res + o);
         }
         float z = 0.f, up = 0.f;
-        for (int j0 = 0; j0 < a.nb; j0 += 128) {
+        for (int j0 = sub; j0 < a.nb; j0 += 4 * WIDTH) {
             float v[4], u[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int j = j0 + 32 * i + lane;
+                const int j = j0 + WIDTH * i;
                 v[i] = j < a.nb ? __ldcg(row + j) : 0.f;
                 if (GATED) u[i] = j < a.nb ? __ldcg(row + a.nb + j) : 0.f;
             }
@@ -534,11 +543,11 @@ __global__ void __launch_bounds__(32 * kDqFinishWarps) k_linear_finish(LinArgs a
             }
         }
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) {
+        for (int s = WIDTH / 2; s > 0; s >>= 1) {
             z += __shfl_xor_sync(0xFFFFFFFFu, z, s);
             if (GATED) up += __shfl_xor_sync(0xFFFFFFFFu, up, s);
         }
-        if (lane == 0) {
+        if (writes) {
             z += zb;
             up += ub;
             float y = q.act == kActNone ? z : lin_activate1(z, q.act);

@@ -174,16 +174,16 @@ __device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u
 
 // The time of a call's tiles of at most `cap` tokens, in ns, and how many ways its last tiles are split.
 // Measured on 74 pairs: a stage of 64 columns takes 0.33 us with 256 tokens and no less than 0.27 us; the
-// epilogue about 0.7 us per 32 tokens, under the next tile's products but for the last; parts of a split
-// tile about 2.5 us more.  Whole tiles go in rounds of all pairs, the rest is split along K while pairs would idle.
+// epilogue 0.6 us and 0.3 us per 32 tokens, under the next tile's products but for the last; parts of a split
+// tile 3 us and 0.4 us per 32 tokens more.  Whole tiles go in rounds of all pairs, the rest is split along K while pairs would idle.
 __device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int &split) {
-    const int stage = max(270, 330 * cap / kLinTokens), ends = 22 * cap;
+    const int stage = max(270, 330 * cap / kLinTokens), ends = 600 + 10 * cap;
     const int rest = tiles % pairs;
     long long ns = (long long)(tiles / pairs) * max(nk * stage, ends) + ends;
     split = 1;
     if (rest) {
         const int ways = max(1, min(pairs / rest, nk / kLpMinSplit));
-        const int whole = nk * stage, parts = (nk + ways - 1) / ways * stage + 2500;
+        const int whole = nk * stage, parts = (nk + ways - 1) / ways * stage + 3000 + 12 * cap;
         split = parts < whole ? ways : 1;
         ns += min(whole, parts);
     }
@@ -465,21 +465,36 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t tlane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t tile = 0;
         bool ok = true;
-        for (int u = pair; u < units; u += pairs, tile++) {
-            const LpUnit x = lp_unit<GROUPED>(a, H, u, nk);
-            const uint32_t b = tile & 1u;
+        // a tile, and the scale and bias of this thread's row in it
+        auto load_row = [&](const LpUnit &x, float &rs, float &bias) {
             const int row = x.row0 + 128 * (int)rank + lrow;   // in workspace order
-            const bool row_in = row < a.lin.rows;
-            float rs = 0.f, bias = 0.f;
-            if (row_in) {
+            rs = bias = 0.f;
+            if (row < a.lin.rows) {
                 rs = __ldg(a.lin.row_scale + (long long)x.group * a.lin.rows + row);
                 if (a.bias)
                     bias = lin_load(static_cast<const T *>(a.bias) + (long long)x.expert * a.lin.rows +
                                     (GATED ? (row >> 1) + (row & 1) * a.lin.half : row));
             }
+        };
+        LpUnit next{};
+        float next_rs = 0.f, next_bias = 0.f;
+        if (pair < units) {
+            next = lp_unit<GROUPED>(a, H, pair, nk);
+            load_row(next, next_rs, next_bias);
+        }
+        for (int u = pair; u < units; u += pairs, tile++) {
+            const LpUnit x = next;
+            const float rs = next_rs, bias = next_bias;
+            const uint32_t b = tile & 1u;
+            const int row = x.row0 + 128 * (int)rank + lrow;
+            const bool row_in = row < a.lin.rows;
             ok = lp_wait(smem_u32(&H.acc_full[b]), (tile >> 1) & 1u, tries) && !*abort_flag;
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (u + pairs < units) {                           // the next tile's row, on its way during this one
+                next = lp_unit<GROUPED>(a, H, u + pairs, nk);
+                load_row(next, next_rs, next_bias);
+            }
             // this warp's chunks of 16 columns: part, part + kLpEach, ...
             const int chunks = (x.t1 - x.t0 + 15) >> 4;
             const uint32_t acc = tlane + b * kLinTokens;
