@@ -62,23 +62,23 @@ size_t dequant_smem(int bits, int out, bool grouped, long long tokens, int nb) {
 }
 int dequant_ctas(int bits) { return bits == 48 ? 1 : bits == 72 ? Dec72::kCtasPerSm : Dec96::kCtasPerSm; }
 
-// Whether a call multiplies its tokens block by block as they are decoded (no decoded weight, no tile
-// product).  Every further token of an expert costs such a call 3.6 ps per block, the other form about 10 us
-// and 48 written bytes per block once: on one matrix of 4096 x 4096, 1 / 2 / 3 / 4 tokens take 29.6 / 32.7 / 35.5 /
-// 38.7 us against 39.2, on 22016 x 4096 three 141 against 148 and four 159.  Over experts what counts is how many
-// tokens one gets: at most one on average (8 tokens, 8 experts of 2816 x 2048: 55 us against 58; over 4 experts 44
-// against 42).
+// Whether a call multiplies its tokens block by block as they are decoded (no decoded weight, no tile product).
+// Every further token of an expert costs such a call 3.6 ps per block, the other form about 10 us and 48
+// written bytes per block once.  Measured on one matrix, with and without a decoded weight: 4096 x 4096, 1 / 2 / 3
+// tokens 27.8 / 30.5 / 33.5 us against 37.4; 22016 x 4096, 1 / 3 tokens 103 / 130 us against 145.  Over experts
+// what counts is how many tokens one gets, two on average: 8 tokens over 4 experts of 2816 x 2048 40.6 us against
+// 41.9, 16 over 8 of 1408 x 1024 27.0 against 27.6.
 //
 // Activations that do not fit in shared memory beside the decoder's tables are restated in the workspace and read
-// through L1: dearer per token, so two tokens of one matrix rather than three (4096 x 11008: 70.8 us against
-// 74.3, three 82.9; one token of 8192 x 28672 287 us against 340; 8 tokens over 64 experts of 1408 x 7168 111
-// against 132).
+// through L1, dearer per token: two tokens of one matrix (4096 x 11008: 70.7 us against 74.5; one of 8192 x 28672
+// 287 against 341), four over as many experts (1408 x 7168: 51 against 59), else one for every fourth expert (16 over
+// 64 of 1408 x 7168 196 against 221, over 16 162 against 121).
 enum Few { kManyTokens, kFewNear, kFewFar };
 Few few_tokens(int bits, bool grouped, int64_t tokens, int experts, int nb) {
-    const int shared = std::min(experts, kLinDots);
-    if (tokens > std::max(3, shared)) return kManyTokens;
+    const int near = std::max(3, experts > 1 ? std::min(2 * experts, kLinDots) : 1);
+    if (tokens > near) return kManyTokens;
     if (dequant_smem(bits, kDqDots, grouped, tokens, nb) <= kSmemLimit / dequant_ctas(bits) - 1024) return kFewNear;
-    return tokens <= std::max(2, shared) ? kFewFar : kManyTokens;
+    return tokens <= std::max({2, std::min(experts, 4), experts / 4}) ? kFewFar : kManyTokens;
 }
 
 // Checks a call (everything but the workspace) and lays out its workspace.

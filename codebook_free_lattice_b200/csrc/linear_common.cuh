@@ -8,11 +8,12 @@
 //
 // runs as two kernels: the blocks are decoded once into an fp16 weight in the caller's workspace
 // (linear_dequant.cuh), and a tile product on the tensor cores multiplies it with every token and
-// applies the epilogue (linear_product.cuh).
+// applies the epilogue (linear_product.cuh).  A few tokens are multiplied with each block as it is
+// decoded, and the second kernel adds the rows up.
 //
 // Scales.  A weight is stored as fp16(w 2^s) with one power of two per row, chosen so that the
-// row's largest gain lies just below the end of the fp16 range: no row, however small or large,
-// meets fp16's subnormals or overflows, and w keeps 11 significant bits.  bf16 activations are
+// row's largest gain lies just below the end of the fp16 range: no row, however small or large its gains, is
+// lost to fp16's subnormals or overflows, and w keeps 11 significant bits.  bf16 activations are
 // restated as fp16(x 2^u) with one power of two per token: 8 significant bits fit in 11, so the
 // restatement is exact down to 2^-28 of the token's largest value and off by at most 2^-39 of it
 // below that, less than the fp32 accumulation of the product rounds.  Both powers leave again in

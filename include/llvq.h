@@ -259,10 +259,11 @@ llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int3
  *   y[t][o] = act(z[t][o])                        + residual[t][o]     gated = 0, o < F = rows
  *   y[t][o] = act(z[t][o]) * z[t][F + o]          + residual[t][o]     gated = 1, o < F = rows / 2
  * (a gated weight holds the gate's rows, then the up projection's).  x, bias, residual and y are of
- * `dtype`; sums, bias, activation and residual are held in fp32 and y is rounded once.  Each decoded
- * weight is rounded to 11 significant bits (fp16 with a power of two per row), for bf16 activations
- * too.  Rows of x and y may have any stride and start at any 2-byte aligned address; rows of y may
- * be the residual's (same address and stride), but not x's.
+ * `dtype`; sums, bias, activation and residual are held in fp32 and y is rounded once.  A few tokens (up to
+ * 3, or 16 over experts) are multiplied block by block with the exact integers, gains in fp32; for more the
+ * weight is decoded into the workspace, each weight rounded to 11 significant bits (fp16 with a power of
+ * two per row), for bf16 activations too.  Rows of x, residual and y may have any stride and start at any
+ * 2-byte aligned address; rows of y may be the residual's (same address and stride), but not x's.
  *
  * llvq_linear: `experts` 0 or 1, `offsets` NULL: tokens rows of x, one matrix.
  * llvq_linear_grouped: `experts` (1 .. 2048) matrices of rows / experts rows each, stacked in w; bias
@@ -288,14 +289,15 @@ typedef struct {
 } llvq_linear_call;
 
 /* Bytes of workspace that a call needs (0 when its sizes or types are refused): the decoded weight of the
- * experts that can have tokens (48 bytes per block), partial sums (19.5 MB on 148 SMs), and for bf16 or
- * unaligned x the activations restated in fp16.  Depends on x's address only by its 16-byte alignment;
- * the sizes and x must be set in `call`, its other pointers need not be.  A call with experts >= 1 is
+ * experts that can have tokens (48 bytes per block), partial sums (19.4 MB on 148 SMs), and for bf16 or
+ * unaligned x the activations restated in fp16; for a few tokens, 4 bytes per block and token.  Depends on
+ * x's address only by its 16-byte alignment; the sizes and x must be set in `call`, its other pointers need
+ * not be.  A call with experts >= 1 is
  * taken as grouped. */
 size_t llvq_linear_workspace(const llvq_codec *codec, const llvq_weight *w, const llvq_linear_call *call);
 
-/* The layer: two launches on `stream` (decode, product with epilogue), no allocation, no synchronisation;
- * the codec's device is made current for the call.  d_workspace: device, 256-byte aligned, owned by the
+/* The layer: two launches on `stream` (decode, then product with epilogue), three where many activations are
+ * restated first; no allocation, no synchronisation.  The codec's device is made current for the call.  d_workspace: device, 256-byte aligned, owned by the
  * caller, contents not kept between calls; calls that may overlap (other streams, graphs replayed at
  * once) each need their own.  cols >= 1; at most 65535 blocks per row.  48-, 72- and 96-bit codecs, both
  * gain modes.  Results do not depend on timing: sums are taken in a fixed order.  An index >= N_M
@@ -319,7 +321,8 @@ const char *llvq_last_error_message(void);
 
 /* Limits of the kernels' bounded waits, for tests of the timeout paths.  The paper has no
  * counterpart.  A kernel waits at most table_polls polls for its table copy into shared memory
- * and at most mma_polls polls for each round of its tensor-core products (tcgen05.mma completion);
+ * and at most mma_polls polls for each round of its tensor-core products (tcgen05.mma completion; a linear
+ * layer's product, whose waits cover a whole tile: 16 times as many);
  * when a wait gives up the kernel raises LLVQ_FLAG_WAIT_TIMEOUT (read by llvq_get_error), skips
  * the rest of its work (its outputs are then unspecified), and before it exits waits again, up to
  * the default limit, for the copy or the products in flight, so that nothing is still writing the

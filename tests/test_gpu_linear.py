@@ -212,8 +212,8 @@ GROUPED = [
     (1, 7, 64, 48, "bfloat16", "silu", True, True, True, "table", "one", 0, 3),
     (9, 40, 130, 333, "float16", "gelu", False, True, True, "table", "each", 2, 1),
     (16, 64, 96, 512, "bfloat16", "silu", True, False, False, "table", "uneven", 0, 0),
-    (16, 20, 34, 2500, "float16", "silu", True, True, True, "table", "uneven", 0, 0),
-    (5, 12, 20, 9001, "bfloat16", "gelu", False, False, False, "direct", "uneven", 4, 7),
+    (16, 70, 34, 2500, "float16", "silu", True, True, True, "table", "uneven", 0, 0),
+    (4, 12, 20, 19001, "bfloat16", "gelu", False, False, False, "direct", "uneven", 4, 7),
     (77, 5, 331, 1000, "float16", "gelu", False, True, True, "direct", "ends", 0, 19),
     (300, 3, 258, 200, "bfloat16", "relu", False, False, True, "table", "one", 5, 0),
     (700, 9, 514, 130, "float16", "gelu_tanh", True, True, True, "table", "uneven", 1, 40),
