@@ -13,10 +13,11 @@ using namespace llvq;
 namespace {
 
 constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
-// Activations of this many values are restated by a kernel of their own, fewer beside the decode, where a warp takes
-// a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096 over 4096 x 4096 133 against 137, 512 over
-// 1024 x 1024 26 against 19 (one more launch).
+// Activations of this many values, or in rows this long, are restated by a kernel of their own, others beside the
+// decode, where a warp takes a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096 over 4096 x 4096 133
+// against 137, 512 over 1024 x 1024 26 against 19 (one more launch).
 constexpr long long kStageValues = 1 << 21;
+constexpr int kStageCols = 4096;
 // A wait of the product covers a whole tile (milliseconds for the longest rows), not one round of few products:
 // 16 times the polls
 constexpr uint32_t kWaitRounds = 16;
@@ -315,7 +316,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     if (!ok) return refuse("sizes or strides beyond a tensor map", LLVQ_ERR_UNSUPPORTED);
     cudaError_t e = cudaSuccess;
     LinArgs first = l;
-    if (l.stage && q->tokens * l.cols >= kStageValues) {
+    if (l.stage && (l.cols > kStageCols || q->tokens * l.cols >= kStageValues)) {
         e = launch_stage(c, l, bf16, (l.cols + 7) / 8, s);
         first.stage = 0;
     }

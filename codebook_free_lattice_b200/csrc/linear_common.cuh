@@ -163,23 +163,6 @@ __device__ __forceinline__ uint4 lin_load8(const uint16_t *row, int i, int n, bo
         if (i + k < n) h[k >> 1] |= (uint32_t)__ldg(row + i + k) << (16 * (k & 1));
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
-// ... or, but for the row's ends, as the two aligned units that hold them, both inside the row, shifted together:
-// for one warp with a long row (139 tokens of 10325 values beside the decode: 60 us against 73).  A row of 1000
-// values, and rows spread over many threads, are faster value by value.
-constexpr int kLinShiftedCols = 4096;
-__device__ __forceinline__ uint4 lin_load8_shifted(const uint16_t *row, int i, int n) {
-    if (i < 8 || i + 16 > n) return lin_load8(row, i, n, false);
-    const unsigned long long at = (unsigned long long)(row + i);
-    const uint4 *p = reinterpret_cast<const uint4 *>(at & ~15ull);
-    const uint4 a = __ldg(p), b = __ldg(p + 1);
-    const uint32_t skip = (uint32_t)at & 15u, half = (skip & 2u) << 3;    // the same for the whole row
-    uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x;
-    if ((skip >> 2) == 1u) { w0 = a.y; w1 = a.z; w2 = a.w; w3 = b.x; w4 = b.y; }
-    if ((skip >> 2) == 2u) { w0 = a.z; w1 = a.w; w2 = b.x; w3 = b.y; w4 = b.z; }
-    if ((skip >> 2) == 3u) { w0 = a.w; w1 = b.x; w2 = b.y; w3 = b.z; w4 = b.w; }
-    return make_uint4(__funnelshift_r(w0, w1, half), __funnelshift_r(w1, w2, half), __funnelshift_r(w2, w3, half),
-                      __funnelshift_r(w3, w4, half));
-}
 
 // The scale of a bf16 token whose largest finite magnitude has these bits: 2^-u, leaving that value in fp16's
 // top binade (subnormals: exponent -126 stands for all of them; 2^126 is the most its inverse can be).
@@ -208,25 +191,23 @@ __device__ __forceinline__ uint32_t lin_top8(uint4 q) {
 
 // One token restated for the product, by one warp: fp16 copied to an aligned row (no scale), bf16 scaled by a
 // power of two and rounded to fp16 (see above).  The row is read twice; the second time it is in L1.
-// SHIFTED: rows that do not start on 16 bytes, by shifted units (long rows) rather than value by value.
-template <bool SHIFTED>
 __device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, int cols, float *scale) {
     const int lane = threadIdx.x & 31;
     const int n8 = (cols + 7) / 8;
     const bool wide = lin_wide(src);
     if (!scale) {
 #pragma unroll 4
-        for (int i = lane; i < n8; i += 32) dst[i] = (SHIFTED ? lin_load8_shifted(src, 8 * i, cols) : lin_load8(src, 8 * i, cols, wide));
+        for (int i = lane; i < n8; i += 32) dst[i] = lin_load8(src, 8 * i, cols, wide);
         return;
     }
     uint32_t top = 0;
 #pragma unroll 4
-    for (int i = lane; i < n8; i += 32) top = max(top, lin_top8((SHIFTED ? lin_load8_shifted(src, 8 * i, cols) : lin_load8(src, 8 * i, cols, wide))));
+    for (int i = lane; i < n8; i += 32) top = max(top, lin_top8(lin_load8(src, 8 * i, cols, wide)));
     top = warp_max(top);
     const float inv = lin_token_scale(top), f = pow2_inverse(inv);
     if (lane == 0) *scale = inv;
 #pragma unroll 4
-    for (int i = lane; i < n8; i += 32) dst[i] = lin_restate8((SHIFTED ? lin_load8_shifted(src, 8 * i, cols) : lin_load8(src, 8 * i, cols, wide)), f);
+    for (int i = lane; i < n8; i += 32) dst[i] = lin_restate8(lin_load8(src, 8 * i, cols, wide), f);
 }
 
 // Many tokens restated by a kernel of their own, one CTA per token, the row held in registers between the scale

@@ -243,11 +243,8 @@ __device__ __forceinline__ void dq_stage(const LinArgs &a, DqShared &H) {
         i = __shfl_sync(0xFFFFFFFFu, i, 0);
         const long long t = lo + blockIdx.x + (long long)i * gridDim.x;
         if (t >= hi) break;
-        const uint16_t *src = static_cast<const uint16_t *>(a.X) + t * a.ldx;
-        uint4 *dst = reinterpret_cast<uint4 *>(a.Xs + t * a.ldxs);
-        float *scale = a.stage == 2 ? a.token_scale + t : nullptr;
-        if (!lin_wide(src) && a.cols > kLinShiftedCols) lin_stage_token<true>(src, dst, a.cols, scale);
-        else lin_stage_token<false>(src, dst, a.cols, scale);
+        lin_stage_token(static_cast<const uint16_t *>(a.X) + t * a.ldx, reinterpret_cast<uint4 *>(a.Xs + t * a.ldxs), a.cols,
+                        a.stage == 2 ? a.token_scale + t : nullptr);
     }
 }
 
