@@ -153,10 +153,14 @@ __device__ __forceinline__ float lin_row_scale(const LinArgs &a, uint32_t top) {
 }
 
 // Eight consecutive 16-bit values from element i (a multiple of 8) of a row of n; elements at and beyond n read
-// as zero.  Rows that do not start on 16 bytes (not wide) are read value by value.
+// as zero.  Rows that do not start on 16 bytes (not wide) are read in pairs or value by value.
 __device__ __forceinline__ bool lin_wide(const uint16_t *row) { return ((unsigned long long)row & 15ull) == 0ull; }
 __device__ __forceinline__ uint4 lin_load8(const uint16_t *row, int i, int n, bool wide) {
     if (wide && i + 8 <= n) return __ldg(reinterpret_cast<const uint4 *>(row + i));
+    if (((unsigned long long)row & 3ull) == 0ull && i + 8 <= n) {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(row + i);
+        return make_uint4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+    }
     uint32_t h[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; k++)

@@ -291,7 +291,7 @@ def test_strides_and_addresses(codecs, tokens, dtype):
     dtype = getattr(torch, dtype)
     layer = Layer(codecs, 48, 90, 203, pitch=13, seed=tokens)
     wide = tokens_of(1, tokens, 350, dtype)
-    for at, width in ((0, 350), (1, 350), (8, 344)):
+    for at, width in ((0, 350), (1, 350), (2, 350), (8, 344)):
         x = wide[:, :width][:, at:at + 203]
         out = random(5, (tokens, 101), dtype)
         kept, r = out.clone(), random(6, (tokens, 97), dtype)
