@@ -48,6 +48,7 @@ struct Plan {
     long long w_pitch = 0, xs_pitch = 0;
     bool far = false;                                      // ... with the activations in the workspace
     bool dots = false;                                     // few tokens: no decoded weight
+    int parts = 1;                                         // LinArgs::parts
     size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
 };
 
@@ -138,7 +139,8 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         p.bytes = at;
         return LLVQ_OK;
     }
-    p.w = place((size_t)p.held * p.w_pitch * sizeof(__half));
+    p.parts = q->gated && q->dtype == LLVQ_DTYPE_FP16 ? lp_parts<true, __half>() : 1;
+    p.w = place((size_t)p.parts * p.held * p.w_pitch * sizeof(__half));
     p.row_scale = place((size_t)p.held * sizeof(float));
     p.counters = place((size_t)c->pairs * kLpCounters * sizeof(unsigned));
     p.partial = place((size_t)c->pairs * 2 * kLinTokens * 128 * sizeof(float));
@@ -272,6 +274,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     l.tokens = q->tokens;
     l.W = (__half *)(ws + p.w);
     l.ldw = p.w_pitch;
+    l.parts = p.parts;
     l.row_scale = (float *)(ws + p.row_scale);
     l.rows_recip = reciprocal((uint32_t)p.rows);
     l.nb_recip = reciprocal((uint32_t)l.nb);
@@ -308,7 +311,8 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     a.partial = (float *)(ws + p.partial);
     a.wait_tries = std::min(g_mma_wait_tries.load(), 1u << 27) * kWaitRounds;
     LpMaps m;
-    bool ok = make_map(m.w, l.W, p.held, l.cols, l.ldw, 128);
+    bool ok = true;
+    for (int i = 0; i < p.parts; i++) ok = ok && make_map(m.w[i], l.W + i * p.held * l.ldw, p.held, l.cols, l.ldw, 128);
     const void *x = p.stage ? (const void *)l.Xs : q->x;
     // the pitch of a single row is never used, but has to be one that a map takes
     const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;

@@ -18,6 +18,12 @@
 // restatement is exact down to 2^-28 of the token's largest value and off by at most 2^-39 of it
 // below that, less than the fp32 accumulation of the product rounds.  Both powers leave again in
 // the epilogue, exactly.  A bf16 weight would have lost 3 bits that fp16 keeps.
+//
+// Against the definition in 64 bits, one fp16 part per weight leaves a bf16 output 1.01 times as far off as its
+// own rounding does, and a plain fp16 output 1.3 times (the weight's rounding is as large as the output's, and
+// independent of it).  A gated fp16 output multiplies two such sums and would be 1.75 times as far off (3.6e-4
+// against 2.1e-4), so its weights have two fp16 parts, the second the rest of the first: 22 bits, 1.00 times,
+// for twice the products and twice the decoded weight.
 #pragma once
 #include <cuda_bf16.h>
 #include "codec48.cuh"
@@ -42,6 +48,7 @@ struct LinArgs {
     // and 1 / (its power of two) per row
     __half *W;
     long long ldw;
+    int parts;                                // fp16 parts of a weight, the second `held` rows behind the first
     float *row_scale;
     uint32_t rows_recip, nb_recip;            // ceil(2^32 / rows), ceil(2^32 / nb) (0 for 1)
     // the split tiles' arrival counters
@@ -307,6 +314,8 @@ __device__ __forceinline__ void lin_activate(float (&z)[N], int act) {
     }
 }
 
+template <class T> struct LinIsBf16 { static constexpr bool value = false; };
+template <> struct LinIsBf16<__nv_bfloat16> { static constexpr bool value = true; };
 template <class T> __device__ __forceinline__ float lin_load(const T *p);
 template <> __device__ __forceinline__ float lin_load<__half>(const __half *p) { return __half2float(*p); }
 template <> __device__ __forceinline__ float lin_load<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }

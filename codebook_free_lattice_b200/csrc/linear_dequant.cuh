@@ -1,6 +1,6 @@
 // linear_dequant.cuh -- the first kernel of a compressed linear layer: every block of the experts
-// that have tokens is decoded once, and written as 24 scaled fp16 weights (linear_common.cuh) or, for a few
-// tokens, multiplied with them at once (k_linear_finish then adds each row's dot products in order).
+// that have tokens is decoded once, and written as 24 scaled fp16 weights (linear_common.cuh; a gated fp16
+// layer's in two parts) or, for a few tokens, multiplied with them at once (k_linear_finish then adds each row's dot products in order).
 //
 // "Leech Lattice Vector Quantization for Efficient LLM Compression", papernotes.org notes,
 // 方法详解 / 关键设计 2: index -> shell, class, codeword, signs, arrangement -> integer vector.
@@ -104,6 +104,28 @@ __device__ __forceinline__ void dq_store(const uint32_t wh[12], float scale, __h
     p[1] = make_uint4(o[4], o[5], o[6], o[7]);
     p[2] = make_uint4(o[8], o[9], o[10], o[11]);
 }
+// The rest of those weights, w - fp16(w), for the second part: v s_hi - fp16(w) is a multiple of s_hi's last
+// place and at most a few of fp16(w)'s, so it is exact, and v s_lo joins it with one rounding.
+template <int GAIN>
+__device__ __forceinline__ void dq_store_rest(const uint32_t wh[12], float scale, __half *out) {
+    const __half hi = __float2half_rn(scale);
+    const __half2 hi2 = __halves2half2(hi, hi);
+    const __half lo = __float2half_rn(scale - __half2float(hi));
+    const __half2 lo2 = __halves2half2(lo, lo);
+    uint32_t o[12];
+#pragma unroll
+    for (int q = 0; q < 12; q++) {
+        const __half2 v = *reinterpret_cast<const __half2 *>(&wh[q]);
+        const __half2 w = GAIN == 0 ? __hmul2(v, hi2) : __hfma2(v, hi2, __hmul2(v, lo2));
+        __half2 rest = __hfma2(v, hi2, __hneg2(w));
+        if (GAIN != 0) rest = __hfma2(v, lo2, rest);
+        o[q] = fabsf(scale) <= 65504.f ? *reinterpret_cast<const uint32_t *>(&rest) : 0u;      // an infinite gain has no rest
+    }
+    uint4 *p = reinterpret_cast<uint4 *>(out);
+    p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    p[2] = make_uint4(o[8], o[9], o[10], o[11]);
+}
 __device__ __forceinline__ void dq_store_zero(__half *out) {
     uint4 *p = reinterpret_cast<uint4 *>(out);
     p[0] = p[1] = p[2] = make_uint4(0u, 0u, 0u, 0u);
@@ -134,7 +156,9 @@ template <int OUT, int GAIN, bool GROUPED>
 __device__ __forceinline__ void dq_block(const LinArgs &a, const DqShared &H, const uint32_t wh[12], float scale, int active,
                                          long long dst, int j) {
     if constexpr (OUT == kDqWeights) {
-        dq_store<GAIN>(wh, scale * pow2_inverse(a.row_scale[dst]), a.W + dst * a.ldw + j * 24);
+        const float s = scale * pow2_inverse(a.row_scale[dst]);
+        dq_store<GAIN>(wh, s, a.W + dst * a.ldw + j * 24);
+        if (a.parts == 2) dq_store_rest<GAIN>(wh, s, a.W + (a.held + dst) * a.ldw + j * 24);
     } else {
         const DqDots &D = *reinterpret_cast<const DqDots *>(H.id);
         const int e = GROUPED ? (int)div_by((uint32_t)active, (uint32_t)a.rows, a.rows_recip) : 0;
@@ -146,6 +170,7 @@ template <int OUT, bool GROUPED>
 __device__ __forceinline__ void dq_no_block(const LinArgs &a, const DqShared &H, int active, long long dst, int j) {
     if constexpr (OUT == kDqWeights) {
         dq_store_zero(a.W + dst * a.ldw + j * 24);
+        if (a.parts == 2) dq_store_zero(a.W + (a.held + dst) * a.ldw + j * 24);
     } else {
         const uint32_t none[12] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
         dq_block<OUT, 0, GROUPED>(a, H, none, 0.f, active, dst, j);

@@ -1,0 +1,54 @@
+"""How near the linear layers come to the definition in 64 bits where a bound per output (test_gpu_linear.py) does not
+show it: the precision of gated layers, the tails of the activations, infinite gains."""
+import pytest
+
+from tests.test_gpu_linear import Layer, activate, codecs, number, random, shares, tokens_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def rms(v):
+    return float(v.double().pow(2).mean().sqrt())
+
+
+def definition(layer, x, act, rows=None):
+    z = x.double() @ (layer.dense if rows is None else layer.dense[rows]).t()
+    half = z.shape[1] // 2
+    return activate(z[:, :half], act) * z[:, half:]
+
+
+# The output's own rounding is the yardstick: its RMS error is measured on the same outputs.  The weights' 22 bits are
+# off by 2^-21 at most, which is nothing beside it.  What is left are the fp32 sums: each of the at most 2 x 63 steps
+# of 16 columns (1000 columns, two parts) takes at most 2^-23 of the running sum, so each of the two sums is off by
+# 2^-16, their product by 2^-15.5 = 2.2e-5, a tenth of the rounding's 2e-4; independent of it, that adds less than 1%.
+# Weights of 11 bits would give 1.7.
+MARGIN = 1.05
+
+
+@pytest.mark.parametrize("bits,tokens,rows,cols,act,gain", [
+    (48, 5, 600, 700, "silu", "table"), (48, 40, 300, 1000, "silu", "direct"), (48, 300, 520, 480, "gelu_tanh", "table"),
+    (72, 50, 130, 300, "none", "table")])
+def test_gated_fp16_is_as_good_as_its_rounding(codecs, bits, tokens, rows, cols, act, gain):
+    layer = Layer(codecs, bits, rows, cols, gain, seed=tokens)
+    x = tokens_of(1, tokens, cols, torch.float16)
+    y = torch.empty(tokens, rows // 2, dtype=torch.float16, device="cuda")
+    layer.codec.linear(layer.weight, x, y, activation=number(act), gated=True)
+    want = definition(layer, x, act)
+    assert rms(y - want) <= MARGIN * rms(want.half() - want)
+    assert layer.codec.get_error() == 0
+
+
+def test_gated_fp16_experts_are_as_good_as_their_rounding(codecs):
+    experts, rows, cols, tokens = 4, 264, 400, 90
+    layer = Layer(codecs, 48, experts * rows, cols, "table", seed=3)
+    x = tokens_of(1, tokens, cols, torch.float16)
+    y = torch.empty(tokens, rows // 2, dtype=torch.float16, device="cuda")
+    counts = shares("uneven", tokens, experts, 5).tolist()
+    edges = [sum(counts[:e]) for e in range(experts + 1)]
+    layer.codec.linear_grouped(layer.weight, experts, x, torch.tensor(edges, dtype=torch.int32, device="cuda"), y,
+                               activation=number("silu"), gated=True)
+    want = torch.cat([definition(layer, x[edges[e]:edges[e + 1]], "silu", slice(e * rows, (e + 1) * rows)) for e in range(experts)])
+    assert rms(y - want) <= MARGIN * rms(want.half() - want)
+    assert layer.codec.get_error() == 0

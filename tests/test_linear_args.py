@@ -196,3 +196,19 @@ def test_binding_matches_the_header(L, bare):
     for name, value in values.items():
         assert getattr(L, name) == int(value, 0), name
     assert C.sizeof(L.llvq_linear_call) == bare["bytes"]
+
+
+@pytest.mark.parametrize("bits", (48, 72, 96))
+def test_workspace_of_a_gated_fp16_layer(L, bare, bits):
+    """Its decoded weight has two fp16 parts; a gated bf16 layer's has one, and so has a few tokens' none."""
+    lib = L.lib()
+
+    def need(**other):
+        w, q = weight(L, 200, 1000, bits), call(L, rows=100, cols=1000, gated=1, **{"tokens": 64, **other})
+        return lib.llvq_linear_workspace(bare[bits], C.byref(w), C.byref(q))
+
+    rest = up256(200 * 4) + up256(74 * 128 * 4) + 74 * 2 * 256 * 128 * 4
+    assert need() == 2 * 200 * 1024 * 2 + rest
+    assert need(experts=4) == 2 * 200 * 1024 * 2 + rest
+    assert need(dtype=1) == 200 * 1024 * 2 + rest + 64 * 1024 * 2 + 256
+    assert need(tokens=2) == up256(2 * 200 * 42 * 4)
