@@ -48,7 +48,7 @@ struct Plan {
     long long w_pitch = 0, xs_pitch = 0;
     bool far = false;                                      // ... with the activations in the workspace
     bool dots = false;                                     // few tokens: no decoded weight
-    int parts = 1;                                         // LinArgs::parts
+    int parts = 1, terms = 0;                              // LinArgs::parts, terms
     size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
 };
 
@@ -120,6 +120,7 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
     // whole 128-byte lines per row: a box row that straddles two lines costs the tensor copies twice
     p.w_pitch = ((long long)w->blocks_per_row * 24 + 63) / 64 * 64;
     p.xs_pitch = ((long long)w->cols + 63) / 64 * 64;
+    p.terms = w->cols;
     size_t at = 0;
     auto place = [&](size_t bytes) {
         const size_t here = at;
@@ -139,8 +140,13 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         p.bytes = at;
         return LLVQ_OK;
     }
-    p.parts = q->gated && q->dtype == LLVQ_DTYPE_FP16 ? lp_parts<true, __half>() : 1;
-    p.w = place((size_t)p.parts * p.held * p.w_pitch * sizeof(__half));
+    if (q->gated && q->dtype == LLVQ_DTYPE_FP16) {
+        p.parts = 2;
+        p.stage = 1;
+        p.terms = w->blocks_per_row * 48;
+        p.w_pitch = p.xs_pitch = ((long long)p.terms + 63) / 64 * 64;
+    }
+    p.w = place((size_t)p.held * p.w_pitch * sizeof(__half));
     p.row_scale = place((size_t)p.held * sizeof(float));
     p.counters = place((size_t)c->pairs * kLpCounters * sizeof(unsigned));
     p.partial = place((size_t)c->pairs * 2 * kLinTokens * 128 * sizeof(float));
@@ -275,6 +281,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     l.W = (__half *)(ws + p.w);
     l.ldw = p.w_pitch;
     l.parts = p.parts;
+    l.terms = p.terms;
     l.row_scale = (float *)(ws + p.row_scale);
     l.rows_recip = reciprocal((uint32_t)p.rows);
     l.nb_recip = reciprocal((uint32_t)l.nb);
@@ -311,20 +318,21 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     a.partial = (float *)(ws + p.partial);
     a.wait_tries = std::min(g_mma_wait_tries.load(), 1u << 27) * kWaitRounds;
     LpMaps m;
-    bool ok = true;
-    for (int i = 0; i < p.parts; i++) ok = ok && make_map(m.w[i], l.W + i * p.held * l.ldw, p.held, l.cols, l.ldw, 128);
+    bool ok = make_map(m.w, l.W, p.held, l.terms, l.ldw, 128);
     const void *x = p.stage ? (const void *)l.Xs : q->x;
     // the pitch of a single row is never used, but has to be one that a map takes
     const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;
-    for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.cols, pitch, 128 >> b);
+    for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.terms, pitch, 128 >> b);
     if (!ok) return refuse("sizes or strides beyond a tensor map", LLVQ_ERR_UNSUPPORTED);
     cudaError_t e = cudaSuccess;
     LinArgs first = l;
     if (l.stage && (l.cols > kStageCols || q->tokens * l.cols >= kStageValues)) {
-        e = launch_stage(c, l, bf16, (l.cols + 7) / 8, s);
+        e = launch_stage(c, l, bf16, p.parts == 2 ? 3 * l.nb : (l.cols + 7) / 8, s);
         first.stage = 0;
     }
-    if (e == cudaSuccess) e = grouped ? launch_dequant<kDqWeights, true>(c, w, first, s) : launch_dequant<kDqWeights, false>(c, w, first, s);
+    if (e == cudaSuccess)
+        e = p.parts == 1 ? (grouped ? launch_dequant<kDqWeights, true>(c, w, first, s) : launch_dequant<kDqWeights, false>(c, w, first, s))
+                         : (grouped ? launch_dequant<kDqTwoParts, true>(c, w, first, s) : launch_dequant<kDqTwoParts, false>(c, w, first, s));
     if (e == cudaSuccess)
         e = grouped ? product_dispatch<true>(c, m, a, q->gated, bf16, s) : product_dispatch<false>(c, m, a, q->gated, bf16, s);
     if (e == cudaSuccess) return LLVQ_OK;
@@ -339,6 +347,10 @@ template <bool GROUPED>
 void allow_all() {
     allow(k_dequant48<kDqWeights, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqWeights, 1, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqTwoParts, 0, GROUPED>, kSmemLimit);
+    allow(k_dequant48<kDqTwoParts, 1, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec72, kDqTwoParts, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec96, kDqTwoParts, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDots, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDots, 1, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDotsFar, 0, GROUPED>, kSmemLimit);

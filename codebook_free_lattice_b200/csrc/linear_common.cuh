@@ -19,11 +19,12 @@
 // below that, less than the fp32 accumulation of the product rounds.  Both powers leave again in
 // the epilogue, exactly.  A bf16 weight would have lost 3 bits that fp16 keeps.
 //
-// Against the definition in 64 bits, one fp16 part per weight leaves a bf16 output 1.01 times as far off as its
+// Against the definition in 64 bits, one fp16 value per weight leaves a bf16 output 1.01 times as far off as its
 // own rounding does, and a plain fp16 output 1.3 times (the weight's rounding is as large as the output's, and
 // independent of it).  A gated fp16 output multiplies two such sums and would be 1.75 times as far off (3.6e-4
-// against 2.1e-4), so its weights have two fp16 parts, the second the rest of the first: 22 bits, 1.00 times,
-// for twice the products and twice the decoded weight.
+// against 2.1e-4), so its weights have two fp16 values, the second the rest of the first: 22 bits, 1.00 times,
+// for twice the products and twice the decoded weight.  A block's 24 values and their 24 rests follow one another,
+// and so do a token's 24 values and the same again: to the product this is one sum over twice the columns.
 #pragma once
 #include <cuda_bf16.h>
 #include "codec48.cuh"
@@ -48,7 +49,8 @@ struct LinArgs {
     // and 1 / (its power of two) per row
     __half *W;
     long long ldw;
-    int parts;                                // fp16 parts of a weight, the second `held` rows behind the first
+    int parts;                                // fp16 values of a weight: 1, or 2 (and of an activation: the same twice)
+    int terms;                                // products of an output: cols, or 48 per block with two parts
     float *row_scale;
     uint32_t rows_recip, nb_recip;            // ceil(2^32 / rows), ceil(2^32 / nb) (0 for 1)
     // the split tiles' arrival counters
@@ -200,12 +202,29 @@ __device__ __forceinline__ uint32_t lin_top8(uint4 q) {
     return top;
 }
 
+// Unit i of 8 values where a block's 3 units are there twice.  An infinity or a NaN is there once: it belongs to the
+// weight, and times the weight's rest (zero, or of the other sign) would make a NaN of an infinity.
+__device__ __forceinline__ uint32_t lin_finite2(uint32_t h) {
+    return h & __hle2_mask(__habs2(*reinterpret_cast<const __half2 *>(&h)), __float2half2_rn(65504.f));
+}
+__device__ __forceinline__ void lin_twice(uint4 *dst, int i, uint4 q) {
+    uint4 *p = dst + i + i / 3 * 3;
+    p[0] = q;
+    p[3] = make_uint4(lin_finite2(q.x), lin_finite2(q.y), lin_finite2(q.z), lin_finite2(q.w));
+}
+
 // One token restated for the product, by one warp: fp16 copied to an aligned row (no scale), bf16 scaled by a
 // power of two and rounded to fp16 (see above).  The row is read twice; the second time it is in L1.
-__device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, int cols, float *scale) {
+// nb > 0: the nb blocks' values twice, for a weight of two parts.
+__device__ __noinline__ void lin_stage_token(const uint16_t *src, uint4 *dst, int cols, int nb, float *scale) {
     const int lane = threadIdx.x & 31;
     const int n8 = (cols + 7) / 8;
     const bool wide = lin_wide(src);
+    if (nb) {
+#pragma unroll 4
+        for (int i = lane; i < 3 * nb; i += 32) lin_twice(dst, i, lin_load8(src, 8 * i, cols, wide));
+        return;
+    }
     if (!scale) {
 #pragma unroll 4
         for (int i = lane; i < n8; i += 32) dst[i] = lin_load8(src, 8 * i, cols, wide);
@@ -267,11 +286,15 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int u
 #pragma unroll
         for (int i = 0; i < kHeld; i++) {
             const int k = tid + threads * i;
-            if (k < n8) dst[k] = BF16 ? lin_restate8(held[i], f) : held[i];
+            if (k < n8) {
+                if (!BF16 && a.parts == 2) lin_twice(dst, k, held[i]);
+                else dst[k] = BF16 ? lin_restate8(held[i], f) : held[i];
+            }
         }
         for (int k = tid + threads * kHeld; k < n8; k += threads) {
             const uint4 q = lin_load8(src, 8 * k, a.cols, wide);
-            dst[k] = BF16 ? lin_restate8(q, f) : q;
+            if (!BF16 && a.parts == 2) lin_twice(dst, k, q);
+            else dst[k] = BF16 ? lin_restate8(q, f) : q;
         }
     }
 }
@@ -314,8 +337,6 @@ __device__ __forceinline__ void lin_activate(float (&z)[N], int act) {
     }
 }
 
-template <class T> struct LinIsBf16 { static constexpr bool value = false; };
-template <> struct LinIsBf16<__nv_bfloat16> { static constexpr bool value = true; };
 template <class T> __device__ __forceinline__ float lin_load(const T *p);
 template <> __device__ __forceinline__ float lin_load<__half>(const __half *p) { return __half2float(*p); }
 template <> __device__ __forceinline__ float lin_load<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }

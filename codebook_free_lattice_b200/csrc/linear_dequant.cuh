@@ -39,7 +39,8 @@ struct DqDots {
     uint32_t top[kLinDots];
     float scale[kLinDots];
 };
-enum DqOut { kDqWeights = 0, kDqDots = 1, kDqDotsFar = 2 };
+enum DqOut { kDqWeights = 0, kDqDots = 1, kDqDotsFar = 2, kDqTwoParts = 3 };
+__host__ __device__ constexpr bool dq_weights(int out) { return out == kDqWeights || out == kDqTwoParts; }
 constexpr size_t kDqHead = 32 + 4 * 32 * sizeof(int) + kDqRare * sizeof(uint4);              // DqShared without its list
 __host__ __device__ constexpr size_t dq_tail(int out, bool grouped, long long tokens, int nb) {
     return kDqHead + (out == kDqDots ? sizeof(DqDots) + (size_t)tokens * nb * 48
@@ -104,31 +105,42 @@ __device__ __forceinline__ void dq_store(const uint32_t wh[12], float scale, __h
     p[1] = make_uint4(o[4], o[5], o[6], o[7]);
     p[2] = make_uint4(o[8], o[9], o[10], o[11]);
 }
-// The rest of those weights, w - fp16(w), for the second part: v s_hi - fp16(w) is a multiple of s_hi's last
-// place and at most a few of fp16(w)'s, so it is exact, and v s_lo joins it with one rounding.
+// 32 bytes at once (32-byte aligned)
+__device__ __forceinline__ void dq_store32(__half *out, const uint32_t *o) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(out), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+}
+// The same weights in two parts, fp16(w) and fp16(w - fp16(w)): v s_hi - fp16(w) is a multiple of s_hi's last place and
+// at most a few of fp16(w)'s, so it is exact, and v s_lo joins it with one rounding.  An infinite gain has no rest.
+// values: coordinates of the block that are columns of the layer.
 template <int GAIN>
-__device__ __forceinline__ void dq_store_rest(const uint32_t wh[12], float scale, __half *out) {
+__device__ __forceinline__ void dq_store_two(const uint32_t wh[12], float scale, int values, __half *out) {
     const __half hi = __float2half_rn(scale);
     const __half2 hi2 = __halves2half2(hi, hi);
     const __half lo = __float2half_rn(scale - __half2float(hi));
     const __half2 lo2 = __halves2half2(lo, lo);
-    uint32_t o[12];
+    const bool finite = fabsf(scale) <= 65504.f;
+    uint32_t o[24];
 #pragma unroll
     for (int q = 0; q < 12; q++) {
         const __half2 v = *reinterpret_cast<const __half2 *>(&wh[q]);
         const __half2 w = GAIN == 0 ? __hmul2(v, hi2) : __hfma2(v, hi2, __hmul2(v, lo2));
         __half2 rest = __hfma2(v, hi2, __hneg2(w));
         if (GAIN != 0) rest = __hfma2(v, lo2, rest);
-        o[q] = fabsf(scale) <= 65504.f ? *reinterpret_cast<const uint32_t *>(&rest) : 0u;      // an infinite gain has no rest
+        o[q] = *reinterpret_cast<const uint32_t *>(&w);
+        o[12 + q] = finite ? *reinterpret_cast<const uint32_t *>(&rest) : 0u;
     }
-    uint4 *p = reinterpret_cast<uint4 *>(out);
-    p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    p[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    p[2] = make_uint4(o[8], o[9], o[10], o[11]);
+#pragma unroll
+    for (int i = 0; i < 3; i++) dq_store32(out + 16 * i, o + 8 * i);
+    // coordinates beyond the columns meet zeros, which an infinity would make a NaN
+    if (!finite)
+        for (int i = values; i < 24; i++) out[i] = __float2half_rn(0.f);
 }
+template <int PARTS>
 __device__ __forceinline__ void dq_store_zero(__half *out) {
     uint4 *p = reinterpret_cast<uint4 *>(out);
-    p[0] = p[1] = p[2] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 3 * PARTS; i++) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // A block's dot products with the tokens of its expert: 24 exact products each, fp32 sums.
@@ -155,10 +167,10 @@ __device__ __forceinline__ void dq_dots(const LinArgs &a, const DqDots &D, const
 template <int OUT, int GAIN, bool GROUPED>
 __device__ __forceinline__ void dq_block(const LinArgs &a, const DqShared &H, const uint32_t wh[12], float scale, int active,
                                          long long dst, int j) {
-    if constexpr (OUT == kDqWeights) {
+    if constexpr (dq_weights(OUT)) {
         const float s = scale * pow2_inverse(a.row_scale[dst]);
-        dq_store<GAIN>(wh, s, a.W + dst * a.ldw + j * 24);
-        if (a.parts == 2) dq_store_rest<GAIN>(wh, s, a.W + (a.held + dst) * a.ldw + j * 24);
+        if constexpr (OUT == kDqWeights) dq_store<GAIN>(wh, s, a.W + dst * a.ldw + j * 24);
+        else dq_store_two<GAIN>(wh, s, a.cols - j * 24, a.W + dst * a.ldw + j * 48);
     } else {
         const DqDots &D = *reinterpret_cast<const DqDots *>(H.id);
         const int e = GROUPED ? (int)div_by((uint32_t)active, (uint32_t)a.rows, a.rows_recip) : 0;
@@ -168,9 +180,9 @@ __device__ __forceinline__ void dq_block(const LinArgs &a, const DqShared &H, co
 // ... and of a block whose index is not coded
 template <int OUT, bool GROUPED>
 __device__ __forceinline__ void dq_no_block(const LinArgs &a, const DqShared &H, int active, long long dst, int j) {
-    if constexpr (OUT == kDqWeights) {
-        dq_store_zero(a.W + dst * a.ldw + j * 24);
-        if (a.parts == 2) dq_store_zero(a.W + (a.held + dst) * a.ldw + j * 24);
+    if constexpr (dq_weights(OUT)) {
+        constexpr int parts = OUT == kDqWeights ? 1 : 2;
+        dq_store_zero<parts>(a.W + dst * a.ldw + j * 24 * parts);
     } else {
         const uint32_t none[12] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
         dq_block<OUT, 0, GROUPED>(a, H, none, 0.f, active, dst, j);
@@ -221,7 +233,7 @@ __device__ __forceinline__ DqRun dq_groups(const LinArgs &a, DqShared &H) {
     if (GROUPED) {
         if (warp == 0) {
             DqDots &D = *reinterpret_cast<DqDots *>(H.id);
-            const int n = OUT != kDqWeights ? lin_groups<true>(a, kLinDots, D.id, D.lo, D.hi)
+            const int n = !dq_weights(OUT) ? lin_groups<true>(a, kLinDots, D.id, D.lo, D.hi)
                                          : lin_groups<false>(a, kLinExperts, H.id, nullptr, nullptr);
             if (lane == 0) H.nact = max(n, 0);
             if (n < 0 && lane == 0 && blockIdx.x == 0) atomicOr(a.flags, LLVQ_FLAG_OFFSETS);
@@ -269,7 +281,7 @@ __device__ __forceinline__ void dq_stage(const LinArgs &a, DqShared &H) {
         const long long t = lo + blockIdx.x + (long long)i * gridDim.x;
         if (t >= hi) break;
         lin_stage_token(static_cast<const uint16_t *>(a.X) + t * a.ldx, reinterpret_cast<uint4 *>(a.Xs + t * a.ldxs), a.cols,
-                        a.stage == 2 ? a.token_scale + t : nullptr);
+                        a.parts == 2 ? a.nb : 0, a.stage == 2 ? a.token_scale + t : nullptr);
     }
 }
 
@@ -358,7 +370,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         return;
     }
     // odd warps restate tokens (memory latency) while the even ones decode (instruction issue)
-    if (OUT == kDqWeights && (warp & 1)) dq_stage<GROUPED>(a, H);
+    if (dq_weights(OUT) && (warp & 1)) dq_stage<GROUPED>(a, H);
 
     bool bad = false;
     int oh = 0, ot = 0, eh = 0, et = 0;       // ring heads and tails (warp-uniform)
@@ -458,7 +470,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dequant48(LinArgs a, Dq48Args
         const int i = 32 * (warp - kDqWarps / 2) + lane;
         if (i < min(H.nrare, kDqRare)) dq48_consume<2, OUT, GAIN, GROUPED>(a, S, H, H.rare[i], run.row0);
     }
-    if (OUT == kDqWeights) dq_stage<GROUPED>(a, H);
+    if (dq_weights(OUT)) dq_stage<GROUPED>(a, H);
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.flags, LLVQ_FLAG_INDEX_RANGE);
 }
 
@@ -476,7 +488,7 @@ __global__ void __launch_bounds__(512, D::kCtasPerSm) k_dequant(LinArgs a, typen
     const DqRun run = dq_groups<OUT, GROUPED>(a, H);
     dq_begin<OUT, GROUPED>(a, H, run);
     __syncthreads();
-    if (OUT == kDqWeights) dq_stage<GROUPED>(a, H);
+    if (dq_weights(OUT)) dq_stage<GROUPED>(a, H);
     bool bad = false;
     for (int t = threadIdx.x; t < run.total; t += blockDim.x) {
         const uint32_t b = (uint32_t)(run.first + t), rl = div_by(b, (uint32_t)a.nb, a.nb_recip);

@@ -23,17 +23,11 @@ namespace llvq {
 constexpr int kLpEpilogueWarps = 16;                       // four per quarter of the TMEM lanes
 constexpr int kLpEach = kLpEpilogueWarps / 4;              // a warp takes every fourth chunk of 16 columns
 constexpr int kLpThreads = 32 * (2 + kLpEpilogueWarps);
+constexpr int kLpStages = 6;
 constexpr int kLpK = 64;                                   // columns of K per stage: one 128-byte swizzle row
 constexpr int kLpABytes = 128 * kLpK * 2;                  // 128 weight rows
 constexpr int kLpBBytes = kLinTokens / 2 * kLpK * 2;       // up to 128 tokens
-// fp16 parts of a weight (linear_common.cuh): each stage then holds both, and both meet the same tokens
-template <bool GATED, class T>
-__host__ __device__ constexpr int lp_parts() { return GATED && !LinIsBf16<T>::value ? 2 : 1; }
-__host__ __device__ constexpr int lp_stage_bytes(int parts) { return parts * kLpABytes + kLpBBytes; }
-__host__ __device__ constexpr int lp_stages(int parts) { return parts == 1 ? 6 : 4; }        // 192 KB either way
-constexpr int kLpStages = lp_stages(1);                    // most
-constexpr int kLpTiles = kLpStages * lp_stage_bytes(1);
-static_assert(lp_stages(2) * lp_stage_bytes(2) <= kLpTiles, "the stages of two parts fit where those of one do");
+constexpr int kLpStageBytes = kLpABytes + kLpBBytes;
 constexpr int kLpBand = 8;                                 // row tiles of a band (L2 reuse of the tokens)
 constexpr int kLpMinSplit = 4;                             // least K stages of a split
 constexpr int kLpCounters = 2 * 4 * 16;                    // per split tile: CTA, warp quarter, chunk of 16 columns
@@ -46,11 +40,11 @@ struct LpShared {
     int id[kLinExperts], lo[kLinExperts], hi[kLinExperts], first[kLinExperts + 1];
 };
 __host__ __device__ constexpr size_t lp_smem(bool grouped) {
-    return 1024 + (size_t)kLpTiles + (grouped ? sizeof(LpShared) : sizeof(LpShared) - 4 * 4 * (kLinExperts - 4));
+    return 1024 + (size_t)kLpStages * kLpStageBytes + (grouped ? sizeof(LpShared) : sizeof(LpShared) - 4 * 4 * (kLinExperts - 4));
 }
 
 struct LpMaps {
-    CUtensorMap w[2];                                      // one per part: boxes of 128 rows x 64 columns
+    CUtensorMap w;                                         // box 128 rows x 64 columns
     CUtensorMap x[4];                                      // boxes of 128, 64, 32, 16 tokens x 64 columns
 };
 struct LpArgs {
@@ -182,8 +176,8 @@ __device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u
 // Measured on 74 pairs: a stage of 64 columns takes 0.33 us with 256 tokens and no less than 0.27 us; the
 // epilogue 0.6 us and 0.3 us per 32 tokens, under the next tile's products but for the last; parts of a split
 // tile 3 us and 0.4 us per 32 tokens more.  Whole tiles go in rounds of all pairs, the rest is split along K while pairs would idle.
-__device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int parts, int &split) {
-    const int stage = parts * max(270, 330 * cap / kLinTokens), ends = 600 + 10 * cap;
+__device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int &split) {
+    const int stage = max(270, 330 * cap / kLinTokens), ends = 600 + 10 * cap;
     const int rest = tiles % pairs;
     long long ns = (long long)(tiles / pairs) * max(nk * stage, ends) + ends;
     split = 1;
@@ -198,7 +192,7 @@ __device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, in
 // The tile size of a call, by one warp: tokens[g] of n groups (in shared memory; or `all` tokens of one).  More
 // and smaller tiles fill idle pairs and shorten the last epilogue, larger ones feed the tensor cores better.
 template <bool GROUPED>
-__device__ __forceinline__ void lp_schedule(LpShared &H, int n, int all, int rt, int pairs, int nk, int parts) {
+__device__ __forceinline__ void lp_schedule(LpShared &H, int n, int all, int rt, int pairs, int nk) {
     const int lane = threadIdx.x & 31, cap = 32 * ((lane & 7) + 1);         // lane i: tiles of 32 (i + 1) tokens
     int tiles = 0;
     if (GROUPED) {
@@ -210,7 +204,7 @@ __device__ __forceinline__ void lp_schedule(LpShared &H, int n, int all, int rt,
     }
     tiles *= rt;
     int split;
-    const int ns = lp_cost(tiles, cap, pairs, nk, parts, split);
+    const int ns = lp_cost(tiles, cap, pairs, nk, split);
     const unsigned best = __ballot_sync(0xFFFFFFFFu, ns == __reduce_min_sync(0xFFFFFFFFu, ns)) & 0xFFu;
     if (lane == 31 - __clz(best)) {                           // larger tiles where times are equal
         H.cap = cap;
@@ -304,14 +298,13 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
     k_linear_product(const __grid_constant__ LpMaps maps, const __grid_constant__ LpArgs a) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    LpShared &H = *reinterpret_cast<LpShared *>(smem_raw + (base - smem_u32(smem_raw)) + kLpTiles);
+    LpShared &H = *reinterpret_cast<LpShared *>(smem_raw + (base - smem_u32(smem_raw)) + kLpStages * kLpStageBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const uint32_t rank = lp_rank();
     const bool leader = rank == 0;
-    constexpr int kParts = lp_parts<GATED, T>(), kStages = lp_stages(kParts), kStage = lp_stage_bytes(kParts);
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const uint32_t tries = a.wait_tries;
-    const int nk = (a.lin.cols + kLpK - 1) / kLpK;
+    const int nk = (a.lin.terms + kLpK - 1) / kLpK;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
@@ -334,8 +327,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
     }
     const int rt = (a.lin.rows + kLinRows - 1) / kLinRows;
     if (warp == 0) {
-        if (lane < 4 + kParts) asm volatile("prefetch.tensormap [%0];" ::"l"(lane < 4 ? &maps.x[lane] : &maps.w[lane - 4]) : "memory");
-        if (!GROUPED) lp_schedule<false>(H, 1, (int)a.lin.tokens, rt, pairs, nk, kParts);
+        if (lane < 5) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.w : &maps.x[lane - 1]) : "memory");
+        if (!GROUPED) lp_schedule<false>(H, 1, (int)a.lin.tokens, rt, pairs, nk);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -347,7 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
         if (warp == 0) {
             const int n = max(lin_groups<true>(a.lin, kLinExperts, H.id, H.lo, H.hi), 0);
             __syncwarp();
-            lp_schedule<true>(H, n, 0, rt, pairs, nk, kParts);
+            lp_schedule<true>(H, n, 0, rt, pairs, nk);
             const int cap = H.cap;
             int tiles = 0;
             for (int g0 = 0; g0 < n; g0 += 32) {              // tiles before each group
@@ -380,24 +373,23 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             const int half = lp_uniform(x.n >> 1), k1 = lp_uniform(x.k1);
             const int wrow = lp_uniform(x.group * a.lin.rows + x.row0 + 128 * (int)rank);
             const int trow = lp_uniform(x.t0 + half * (int)rank);
-            const uint32_t bytes = 2u * (uint32_t)(kParts * kLpABytes + half * kLpK * 2);
+            const uint32_t bytes = 2u * (uint32_t)(kLpABytes + half * kLpK * 2);
             for (int k = lp_uniform(x.k0); k < k1; k++) {
                 ok = lp_wait(empty0 + 8 * s, phase, tries);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                const uint32_t st = base + s * kStage, tok = st + kParts * kLpABytes, bar = full0 + 8 * s;
+                const uint32_t st = base + s * kLpStageBytes, bar = full0 + 8 * s;
                 if (lp_elect()) {
                     if (leader)
                         asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-#pragma unroll
-                    for (int p = 0; p < kParts; p++) lp_load(st + p * kLpABytes, &maps.w[p], k * kLpK, wrow, bar);
+                    lp_load(st, &maps.w, k * kLpK, wrow, bar);
                     if (half == 128) {
-                        lp_load(tok, &maps.x[0], k * kLpK, trow, bar);
+                        lp_load(st + kLpABytes, &maps.x[0], k * kLpK, trow, bar);
                     } else {
                         int at = 0;
 #pragma unroll
                         for (int b = 1; b < 4; b++) {
                             if (half & (128 >> b)) {
-                                lp_load(tok + at * kLpK * 2, &maps.x[b], k * kLpK, trow + at, bar);
+                                lp_load(st + kLpABytes + at * kLpK * 2, &maps.x[b], k * kLpK, trow + at, bar);
                                 at += 128 >> b;
                             }
                         }
@@ -405,20 +397,20 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 __syncwarp();
                 issued++;
-                if (++s == kStages) { s = 0; phase ^= 1u; }
+                if (++s == kLpStages) { s = 0; phase ^= 1u; }
             }
         }
         // the last products' releases of the stages must have arrived before this CTA may leave
-        for (uint32_t back = min(issued, (uint32_t)kStages); ok && back > 0; back--) {
+        for (uint32_t back = min(issued, (uint32_t)kLpStages); ok && back > 0; back--) {
             const uint32_t i = issued - back;
-            ok = lp_wait(empty0 + 8 * (i % kStages), (i / kStages) & 1u, tries);
+            ok = lp_wait(empty0 + 8 * (i % kLpStages), (i / kLpStages) & 1u, tries);
         }
         if (!ok) *abort_flag = 1;
         // copies still under way after a wait gave up: the leader waits for the last of each stage
         if (leader && !ok)
-            for (uint32_t back = 1; back <= min(issued, (uint32_t)kStages); back++) {
+            for (uint32_t back = 1; back <= min(issued, (uint32_t)kLpStages); back++) {
                 const uint32_t i = issued - back;
-                lp_wait(smem_u32(&H.full[i % kStages]), (i / kStages) & 1u, kBulkWaitTries);
+                lp_wait(smem_u32(&H.full[i % kLpStages]), (i / kLpStages) & 1u, kBulkWaitTries);
             }
     } else if (warp == 1) {
         if (leader) {
@@ -439,21 +431,19 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                     ok = lp_wait(full0 + 8 * s, phase, tries);
                     if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint64_t ad = lp_desc(base + s * kStage), bd = lp_desc(base + s * kStage + kParts * kLpABytes);
+                    const uint64_t ad = lp_desc(base + s * kLpStageBytes), bd = lp_desc(base + s * kLpStageBytes + kLpABytes);
                     if (lp_elect()) {
 #pragma unroll
-                        for (int i = 0; i < kParts * (kLpK / 16); i++) {
-                            const int p = i / (kLpK / 16), q = i % (kLpK / 16);       // 16 columns are 32 bytes along the swizzled row
+                        for (int q = 0; q < kLpK / 16; q++)       // 16 columns are 32 bytes along the swizzled row
                             asm volatile(
                                 "{\n\t.reg .pred p;\n\t"
                                 "setp.ne.b32 p, %4, 0;\n\t"
                                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                                ::"r"(d), "l"(ad + p * (kLpABytes >> 4) + 2 * q), "l"(bd + 2 * q), "r"(idesc), "r"((uint32_t)(k > k0 || i > 0)));
-                        }
+                                ::"r"(d), "l"(ad + 2 * q), "l"(bd + 2 * q), "r"(idesc), "r"((uint32_t)(k > k0 || q > 0)));
                         lp_commit(empty0 + 8 * s);
                     }
                     __syncwarp();
-                    if (++s == kStages) { s = 0; phase ^= 1u; }
+                    if (++s == kLpStages) { s = 0; phase ^= 1u; }
                 }
                 if (ok && lp_elect()) lp_commit(smem_u32(&H.acc_full[b]));
                 __syncwarp();

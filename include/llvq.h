@@ -263,7 +263,7 @@ llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int3
  * 3, or 16 over experts) are multiplied block by block with the exact integers, gains in fp32; for more the
  * weight is decoded into the workspace, each weight rounded to 11 significant bits (fp16 with a power of
  * two per row), for bf16 activations too; a gated fp16 layer, which multiplies two sums, keeps 22 bits in two
- * fp16 parts, at twice the products.  Rows of x, residual and y may have any stride and start at any
+ * fp16 values, at twice the products.  Rows of x, residual and y may have any stride and start at any
  * 2-byte aligned address; rows of y may be the residual's (same address and stride), but not x's.
  *
  * llvq_linear: `experts` 0 or 1, `offsets` NULL: tokens rows of x, one matrix.
@@ -290,8 +290,8 @@ typedef struct {
 } llvq_linear_call;
 
 /* Bytes of workspace that a call needs (0 when its sizes or types are refused): the decoded weight of the
- * experts that can have tokens (48 bytes per block, 96 for gated fp16), partial sums (19.4 MB on 148 SMs), and for bf16 or
- * unaligned x the activations restated in fp16; for a few tokens, 4 bytes per block and token.  Depends on
+ * experts that can have tokens (48 bytes per block, 96 for gated fp16), partial sums (19.4 MB on 148 SMs), and for
+ * bf16 or unaligned x the activations restated in fp16 (for gated fp16 twice over); for a few tokens, 4 bytes per block and token.  Depends on
  * x's address only by its 16-byte alignment; the sizes and x must be set in `call`, its other pointers need
  * not be.  A call with experts >= 1 is
  * taken as grouped. */

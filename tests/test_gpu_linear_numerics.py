@@ -52,3 +52,24 @@ def test_gated_fp16_experts_are_as_good_as_their_rounding(codecs):
     want = torch.cat([definition(layer, x[edges[e]:edges[e + 1]], "silu", slice(e * rows, (e + 1) * rows)) for e in range(experts)])
     assert rms(y - want) <= MARGIN * rms(want.half() - want)
     assert layer.codec.get_error() == 0
+
+
+@pytest.mark.parametrize("gain", ("table", "direct"))
+@pytest.mark.parametrize("tokens,cols", ((40, 150), (600, 4001)))
+def test_infinities_in_a_gated_fp16_layer(codecs, tokens, cols, gain):
+    """Where the definition has an infinity, a NaN or a number, so has the layer: x with infinities and a NaN, a row
+    with a NaN among its gains (its last block, beyond whose columns the layer has none)."""
+    layer = Layer(codecs, 48, 130, cols, gain, seed=4)
+    x = tokens_of(1, tokens, cols, torch.float16)
+    x[1, 7], x[2, 3], x[3, cols - 1] = float("nan"), float("inf"), -float("inf")
+    y = torch.empty(tokens, 65, dtype=torch.float16, device="cuda")
+    layer.codec.linear(layer.weight, x, y, gated=True)
+    want = definition(layer, x, "none")
+    assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
+    assert torch.equal(y[want.isinf()] > 0, want[want.isinf()] > 0)
+    assert bool(want.isinf().any()) and layer.codec.get_error() == 0
+    g = layer.gains_d.view(torch.float16)
+    g[5] = float("nan")
+    x = tokens_of(1, tokens, cols, torch.float16)
+    layer.codec.linear(layer.weight, x, y, gated=True)
+    assert bool(y[:, 5].isnan().all()) and int(y.isnan().sum()) == tokens

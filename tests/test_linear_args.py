@@ -200,7 +200,8 @@ def test_binding_matches_the_header(L, bare):
 
 @pytest.mark.parametrize("bits", (48, 72, 96))
 def test_workspace_of_a_gated_fp16_layer(L, bare, bits):
-    """Its decoded weight has two fp16 parts; a gated bf16 layer's has one, and so has a few tokens' none."""
+    """Its decoded weight has two fp16 values per weight, and so have its activations; a gated bf16 layer's has one, and
+    a few tokens need the dot products alone."""
     lib = L.lib()
 
     def need(**other):
@@ -208,7 +209,6 @@ def test_workspace_of_a_gated_fp16_layer(L, bare, bits):
         return lib.llvq_linear_workspace(bare[bits], C.byref(w), C.byref(q))
 
     rest = up256(200 * 4) + up256(74 * 128 * 4) + 74 * 2 * 256 * 128 * 4
-    assert need() == 2 * 200 * 1024 * 2 + rest
-    assert need(experts=4) == 2 * 200 * 1024 * 2 + rest
+    assert need() == need(x_stride=1003) == need(experts=4) == 200 * 2048 * 2 + rest + 64 * 2048 * 2      # 42 blocks of 48
     assert need(dtype=1) == 200 * 1024 * 2 + rest + 64 * 1024 * 2 + 256
     assert need(tokens=2) == up256(2 * 200 * 42 * 4)
