@@ -84,6 +84,11 @@ __device__ __forceinline__ void dq_row(const LinArgs &a, const int *id, int acti
     }
 }
 
+// What fp16(scale) leaves of a block's scale; nothing of an infinite one (the difference would be a NaN).
+__device__ __forceinline__ __half dq_rest(float scale, __half hi) {
+    return __float2half_rn(fabsf(scale) <= 65504.f ? scale - __half2float(hi) : 0.f);
+}
+
 // 24 integers (12 exact fp16 pairs) times the block's scale, each rounded once to fp16.  Direct gains
 // times a power of two are fp16 values, one product.  A table gain over |v| is not: its rounding
 // error goes in as a second factor, w = v s_hi + (v s_lo), so that the sum is rounded once.
@@ -91,7 +96,7 @@ template <int GAIN>
 __device__ __forceinline__ void dq_store(const uint32_t wh[12], float scale, __half *out) {
     const __half hi = __float2half_rn(scale);
     const __half2 hi2 = __halves2half2(hi, hi);
-    const __half lo = __float2half_rn(scale - __half2float(hi));
+    const __half lo = dq_rest(scale, hi);
     const __half2 lo2 = __halves2half2(lo, lo);
     uint32_t o[12];
 #pragma unroll
@@ -117,7 +122,7 @@ template <int GAIN>
 __device__ __forceinline__ void dq_store_two(const uint32_t wh[12], float scale, int values, __half *out) {
     const __half hi = __float2half_rn(scale);
     const __half2 hi2 = __halves2half2(hi, hi);
-    const __half lo = __float2half_rn(scale - __half2float(hi));
+    const __half lo = dq_rest(scale, hi);
     const __half2 lo2 = __halves2half2(lo, lo);
     const bool finite = fabsf(scale) <= 65504.f;
     uint32_t o[24];

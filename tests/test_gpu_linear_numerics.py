@@ -73,3 +73,34 @@ def test_infinities_in_a_gated_fp16_layer(codecs, tokens, cols, gain):
     x = tokens_of(1, tokens, cols, torch.float16)
     layer.codec.linear(layer.weight, x, y, gated=True)
     assert bool(y[:, 5].isnan().all()) and int(y.isnan().sum()) == tokens
+
+
+@pytest.mark.parametrize("gain", ("table", "direct"))
+@pytest.mark.parametrize("tokens,dtype,gated", ((2, "float16", False), (40, "float16", False), (40, "bfloat16", False), (40, "float16", True)))
+def test_infinite_gains(codecs, tokens, dtype, gated, gain):
+    """A row with an infinite gain at one block: the layer has an infinity where the definition has one (the products
+    of the block all of one sign), of the same sign, and a NaN where it has one."""
+    dtype = getattr(torch, dtype)
+    layer = Layer(codecs, 48, 64, 60, gain, seed=9)         # 2.5 blocks per row
+    row = next(r for r in range(32) if bool((layer.dense[r, :24] != 0).all()))       # an odd block: no coordinate is zero
+    x = tokens_of(1, tokens, 60, dtype)
+    sign = torch.sign(layer.dense[row, :24]).to(dtype)
+    x[0, :24], x[1, :24] = sign * x[0, :24].abs(), -sign * x[1, :24].abs()
+    infinite = torch.zeros(64, 60, dtype=torch.float64, device="cuda")
+    g = layer.gains_d.view(torch.float16)
+    if gain == "direct":
+        g[row, 0] = float("inf")
+    else:
+        code = int(layer.words_d.reshape(64, -1)[row, 0] >> 48) & 255
+        g[row, code] = float("inf")
+        assert all(int(w >> 48) & 255 != code for w in layer.words_d.reshape(64, -1)[row, 1:])
+    infinite[row, :24] = float("inf")
+    layer.dense = torch.where(infinite > 0, torch.sign(layer.dense) * infinite, layer.dense)
+    y = torch.empty(tokens, 32 if gated else 64, dtype=dtype, device="cuda")
+    layer.codec.linear(layer.weight, x, y, gated=gated)
+    want = definition(layer, x, "none") if gated else x.double() @ layer.dense.t()
+    assert bool(want[:2, row].isinf().all())
+    finite = want.isfinite()
+    assert torch.equal(y.isfinite(), finite)
+    some = want.isinf()
+    assert torch.equal(y[some].double(), want[some])
