@@ -300,22 +300,14 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int u
 }
 
 // Activations, four values at a time and out of line: the code of one activation is fetched once, and
-// a kernel that needs none of it does not step over it.  Each is written so that its negative tail keeps
-// its accuracy: z / (1 + e^-u), and for gelu the complementary error function by the rational
-// approximation 7.1.26 of Abramowitz and Stegun, erfc(x) = t (a1 + t (a2 + ...)) e^-x^2 with t = 1 / (1 + p x),
-// off by at most 1.5e-7 (a fifth of the instructions of erfcf, whose last bits a 16-bit output drops).
+// a kernel that needs none of it does not step over it.  Each keeps the relative accuracy of its negative tail,
+// which a gate can bring back: z P(z) with P(z) = erfc(-z / sqrt 2) / 2 for gelu, and z / (1 + e^-u) for the others.
 // The quick division and exponential are good to a few fp32 steps; a denominator beyond 2^126 gives 0, the limit.
 enum LinAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 __device__ __forceinline__ float lin_activate1(float z, int act) {
     if (act == kActRelu) return z < 0.f ? 0.f : z;                              // NaN stays
     if (act == kActGelu) {
-        const float x = fabsf(z) * 0.70710678118654752f;
-        const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-        float q = fmaf(1.061405429f, t, -1.453152027f);
-        q = fmaf(q, t, 1.421413741f);
-        q = fmaf(q, t, -0.284496736f);
-        q = fmaf(q, t, 0.254829592f);
-        const float tail = 0.5f * q * t * __expf(-x * x);                       // P(|z|): z or less at -|z|
+        const float tail = 0.5f * erfcf(fabsf(z) * 0.70710678118654752f);       // P(-|z|)
         return z * (z < 0.f ? tail : 1.f - tail);
     }
     const float u = act == kActSilu ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);     // 2 sqrt(2 / pi)

@@ -104,3 +104,32 @@ def test_infinite_gains(codecs, tokens, dtype, gated, gain):
     assert torch.equal(y.isfinite(), finite)
     some = want.isinf()
     assert torch.equal(y[some].double(), want[some])
+
+
+@pytest.mark.parametrize("dtype", ("float16", "bfloat16"))
+@pytest.mark.parametrize("tokens", (1, 40))
+@pytest.mark.parametrize("gated", (False, True))
+@pytest.mark.parametrize("act,low", (("gelu", -12.5),))
+def test_tails_of_the_activations(codecs, act, low, gated, tokens, dtype):
+    """z from the bias alone (every gain is zero), so that it is exact: the activation is as good as its rounding, relative
+    to its value, as far as the type goes; a gated layer's factor of 512 brings more of an fp16 tail back.
+
+    The evaluation, with fp32's half step h = 2^-24 and |u| <= 88.5 the exponent: the exponential is off by 2 h (2 + 1.16
+    |u|) <= 2^-16.2; its argument's three roundings by 3 h |u| <= 2^-15.9 more (gelu: erfc by 8 h, and its argument's by
+    2 h z^2 / 2 <= 2^-16.7); the rest are a few h.  Together below 2^-14.9; 2^-14 is allowed."""
+    dtype = getattr(torch, dtype)
+    values = 400
+    layer = Layer(codecs, 48, values * (2 if gated else 1), 30, seed=1)
+    layer.gains_d.zero_()
+    z = torch.linspace(low, 8, values, device="cuda").to(dtype)
+    bias = torch.cat((z, torch.full_like(z, 512))) if gated else z
+    x = tokens_of(1, tokens, 30, dtype)
+    y = torch.empty(tokens, values, dtype=dtype, device="cuda")
+    layer.codec.linear(layer.weight, x, y, bias=bias, activation=number(act), gated=gated)
+    # (1 + erf) / 2, or ndtr where it is computed so, has no tail in 64 bits either; erfc has
+    want = z.double() * torch.special.erfc(z.double() / -2 ** 0.5) / 2 if act == "gelu" else activate(z.double(), act)
+    want *= 512 if gated else 1
+    u = torch.finfo(dtype).eps / 2
+    err = (y.double() - want).abs()
+    bound = (u + 2.0 ** -14) * want.abs() + torch.finfo(dtype).tiny * u
+    assert bool((err <= bound).all()), f"worst error {float((err / bound).max()):.3g} of its bound at z = {float(z[(err / bound).amax(0).argmax()])}"
