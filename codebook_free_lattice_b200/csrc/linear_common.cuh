@@ -301,8 +301,10 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int u
 
 // Activations, four values at a time and out of line: the code of one activation is fetched once, and
 // a kernel that needs none of it does not step over it.  Each keeps the relative accuracy of its negative tail,
-// which a gate can bring back: z P(z) with P(z) = erfc(-z / sqrt 2) / 2 for gelu, and z / (1 + e^-u) for the others.
-// The quick division and exponential are good to a few fp32 steps; a denominator beyond 2^126 gives 0, the limit.
+// which a gate can bring back: z P(z) with P(z) = erfc(-z / sqrt 2) / 2 for gelu, and z e^u / (1 + e^u) below
+// zero for the others, so that the denominator lies between 1 and 2.  The quick division is good to a few fp32 steps,
+// the quick exponential to 1.2 |u| more: 2^-16 where e^u is about to leave fp32's range, an eighth of a 16-bit
+// half step.
 enum LinAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 __device__ __forceinline__ float lin_activate1(float z, int act) {
     if (act == kActRelu) return z < 0.f ? 0.f : z;                              // NaN stays
@@ -311,7 +313,8 @@ __device__ __forceinline__ float lin_activate1(float z, int act) {
         return z * (z < 0.f ? tail : 1.f - tail);
     }
     const float u = act == kActSilu ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);     // 2 sqrt(2 / pi)
-    return __fdividef(z, 1.f + __expf(-u));
+    const float e = __expf(-fabsf(u));
+    return __fdividef(u < 0.f ? z * e : z, 1.f + e);
 }
 __device__ __noinline__ float4 lin_activate4(float4 z, int act) {
     return make_float4(lin_activate1(z.x, act), lin_activate1(z.y, act), lin_activate1(z.z, act), lin_activate1(z.w, act));

@@ -109,7 +109,7 @@ def test_infinite_gains(codecs, tokens, dtype, gated, gain):
 @pytest.mark.parametrize("dtype", ("float16", "bfloat16"))
 @pytest.mark.parametrize("tokens", (1, 40))
 @pytest.mark.parametrize("gated", (False, True))
-@pytest.mark.parametrize("act,low", (("gelu", -12.5),))
+@pytest.mark.parametrize("act,low", (("silu", -88.0), ("gelu_tanh", -9.75), ("gelu", -12.5)))
 def test_tails_of_the_activations(codecs, act, low, gated, tokens, dtype):
     """z from the bias alone (every gain is zero), so that it is exact: the activation is as good as its rounding, relative
     to its value, as far as the type goes; a gated layer's factor of 512 brings more of an fp16 tail back.
