@@ -31,6 +31,12 @@
 
 namespace llvq {
 
+// Loads.  A layer's kernels start before the ones ahead of them on the stream have ended (griddepcontrol), so what
+// those write is written while the reader is alive: the workspace, but also x, the residual and the offsets,
+// which may be another layer's outputs.  They are read by coherent loads after griddepcontrol.wait (__ldca, __ldcg,
+// plain ones), never by __ldg, whose loads promise nothing for such data.  The weight's words and gains and the
+// codec's tables are not written while a layer may run, and take __ldg.
+
 constexpr int kLinExperts = 2048;             // most experts of one call (their groups sit in shared memory)
 constexpr int kLinRows = 256;                 // weight rows of a tile (one pair of CTAs)
 constexpr int kLinTokens = 256;               // most tokens of a tile
@@ -97,8 +103,8 @@ __device__ __forceinline__ int lin_groups(const LinArgs &a, int room, int *id, i
         const int e = e0 + lane;
         int s = 0, t = 0;
         if (e < a.experts) {
-            s = __ldg(a.offsets + e);
-            t = __ldg(a.offsets + e + 1);
+            s = __ldca(a.offsets + e);
+            t = __ldca(a.offsets + e + 1);
             bad |= t < s || s < 0 || (long long)t > a.tokens;
         }
         const unsigned m = __ballot_sync(0xFFFFFFFFu, t > s);
@@ -165,15 +171,15 @@ __device__ __forceinline__ float lin_row_scale(const LinArgs &a, uint32_t top) {
 // as zero.  Rows that do not start on 16 bytes (not wide) are read in pairs or value by value.
 __device__ __forceinline__ bool lin_wide(const uint16_t *row) { return ((unsigned long long)row & 15ull) == 0ull; }
 __device__ __forceinline__ uint4 lin_load8(const uint16_t *row, int i, int n, bool wide) {
-    if (wide && i + 8 <= n) return __ldg(reinterpret_cast<const uint4 *>(row + i));
+    if (wide && i + 8 <= n) return __ldca(reinterpret_cast<const uint4 *>(row + i));
     if (((unsigned long long)row & 3ull) == 0ull && i + 8 <= n) {
         const uint32_t *p = reinterpret_cast<const uint32_t *>(row + i);
-        return make_uint4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+        return make_uint4(__ldca(p), __ldca(p + 1), __ldca(p + 2), __ldca(p + 3));
     }
     uint32_t h[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; k++)
-        if (i + k < n) h[k >> 1] |= (uint32_t)__ldg(row + i + k) << (16 * (k & 1));
+        if (i + k < n) h[k >> 1] |= (uint32_t)__ldca(row + i + k) << (16 * (k & 1));
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int u
     const int tid = threadIdx.x, threads = blockDim.x;
     long long lo = 0, hi = a.tokens;
     if (a.offsets) {                          // rows that no group has are not read; bad offsets are the decode's to tell
-        lo = max(0, __ldg(a.offsets));
-        hi = min(a.tokens, (long long)__ldg(a.offsets + a.experts));
+        lo = max(0, __ldca(a.offsets));
+        hi = min(a.tokens, (long long)__ldca(a.offsets + a.experts));
     }
     const int n8 = units;
     int turn = 0;

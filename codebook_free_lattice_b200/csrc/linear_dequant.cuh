@@ -158,7 +158,7 @@ __device__ __forceinline__ void dq_dots(const LinArgs &a, const DqDots &D, const
         float d0 = 0.f, d1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 3; c++) {
-            const uint4 q = OUT == kDqDots ? xt[c] : __ldg(xt + c);
+            const uint4 q = OUT == kDqDots ? xt[c] : __ldca(xt + c);
             d0 = fma2_f16_f32(wh[4 * c + 0], q.x, d0);
             d1 = fma2_f16_f32(wh[4 * c + 1], q.y, d1);
             d0 = fma2_f16_f32(wh[4 * c + 2], q.z, d0);
@@ -256,7 +256,7 @@ __device__ __forceinline__ void dq_begin(const LinArgs &a, DqShared &H, const Dq
         return;
     }
     if constexpr (OUT == kDqDotsFar) {
-        if (threadIdx.x < a.tokens) reinterpret_cast<DqDots *>(H.id)->scale[threadIdx.x] = a.bf16 ? __ldg(a.token_scale + threadIdx.x) : 1.f;
+        if (threadIdx.x < a.tokens) reinterpret_cast<DqDots *>(H.id)->scale[threadIdx.x] = a.bf16 ? __ldcg(a.token_scale + threadIdx.x) : 1.f;
         return;
     }
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x) a.counters[i] = 0u;
@@ -276,8 +276,8 @@ __device__ __forceinline__ void dq_stage(const LinArgs &a, DqShared &H) {
     long long lo = 0, hi = a.tokens;
     if (GROUPED) {
         if (H.nact == 0) return;
-        lo = __ldg(a.offsets);
-        hi = __ldg(a.offsets + a.experts);
+        lo = __ldca(a.offsets);
+        hi = __ldca(a.offsets + a.experts);
     }
     while (true) {
         int i = 0;

@@ -242,7 +242,7 @@ __device__ __forceinline__ void lp_load_ends(const LpArgs &a, LpEnds<GATED, T> &
             res += step;
         }
     }
-    if (a.lin.stage == 2) e.scale = lane < min(16, t1 - t) ? __ldg(a.lin.token_scale + t + lane) : 0.f;
+    if (a.lin.stage == 2) e.scale = lane < min(16, t1 - t) ? __ldcg(a.lin.token_scale + t + lane) : 0.f;
 }
 
 // The outputs of a chunk of this thread's weight row, from its accumulators.  Addresses step from token to
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             const int row = x.row0 + 128 * (int)rank + lrow;   // in workspace order
             rs = bias = 0.f;
             if (row < a.lin.rows) {
-                rs = __ldg(a.lin.row_scale + (long long)x.group * a.lin.rows + row);
+                rs = __ldcg(a.lin.row_scale + (long long)x.group * a.lin.rows + row);
                 if (a.bias)
                     bias = lin_load(static_cast<const T *>(a.bias) + (long long)x.expert * a.lin.rows +
                                     (GATED ? (row >> 1) + (row & 1) * a.lin.half : row));
