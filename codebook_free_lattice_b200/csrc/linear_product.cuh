@@ -35,7 +35,8 @@ constexpr int kLpCounters = 2 * 4 * 16;                    // per split tile: CT
 struct LpShared {
     unsigned long long full[kLpStages], empty[kLpStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
-    int abort, nact, pad;
+    int abort, nact;
+    uint32_t issued, bytes[kLpStages];                     // stages that this CTA has loaded, and of how many bytes
     int whole, split, units, cap;
     int id[kLinExperts], lo[kLinExperts], hi[kLinExperts], first[kLinExperts + 1];
 };
@@ -81,6 +82,21 @@ __device__ __forceinline__ uint32_t lp_leader(uint32_t addr) {
 }
 __device__ __forceinline__ void lp_init_barrier(uint32_t bar, uint32_t arrivals) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(arrivals) : "memory");
+}
+// A wait gave up: both CTAs are to stop.
+__device__ __forceinline__ uint32_t lp_peer(uint32_t addr) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(lp_rank() ^ 1u));
+    return r;
+}
+__device__ __forceinline__ void lp_abort(LpShared &H) {
+    *(volatile int *)&H.abort = 1;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(lp_peer(smem_u32(&H.abort))), "r"(1) : "memory");
+}
+__device__ __forceinline__ uint32_t lp_of_peer(const uint32_t &word) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(lp_peer(smem_u32(&word))) : "memory");
+    return v;
 }
 // bounded wait; false when it gave up
 __device__ __forceinline__ bool lp_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
@@ -373,14 +389,15 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             const int half = lp_uniform(x.n >> 1), k1 = lp_uniform(x.k1);
             const int wrow = lp_uniform(x.group * a.lin.rows + x.row0 + 128 * (int)rank);
             const int trow = lp_uniform(x.t0 + half * (int)rank);
-            const uint32_t bytes = 2u * (uint32_t)(kLpABytes + half * kLpK * 2);
+            const uint32_t bytes = (uint32_t)(kLpABytes + half * kLpK * 2);          // of each CTA
             for (int k = lp_uniform(x.k0); k < k1; k++) {
                 ok = lp_wait(empty0 + 8 * s, phase, tries);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 const uint32_t st = base + s * kLpStageBytes, bar = full0 + 8 * s;
                 if (lp_elect()) {
                     if (leader)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(2u * bytes) : "memory");
+                    H.bytes[s] = bytes;
                     lp_load(st, &maps.w, k * kLpK, wrow, bar);
                     if (half == 128) {
                         lp_load(st + kLpABytes, &maps.x[0], k * kLpK, trow, bar);
@@ -405,13 +422,11 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t i = issued - back;
             ok = lp_wait(empty0 + 8 * (i % kLpStages), (i / kLpStages) & 1u, tries);
         }
-        if (!ok) *abort_flag = 1;
-        // copies still under way after a wait gave up: the leader waits for the last of each stage
-        if (leader && !ok)
-            for (uint32_t back = 1; back <= min(issued, (uint32_t)kLpStages); back++) {
-                const uint32_t i = issued - back;
-                lp_wait(smem_u32(&H.full[i % kLpStages]), (i / kLpStages) & 1u, kBulkWaitTries);
-            }
+        if (lane == 0) {
+            H.issued = issued;
+            if (!ok) lp_abort(H);
+        }
+        __syncwarp();
     } else if (warp == 1) {
         if (leader) {
             // ---- products: one thread issues for both CTAs
@@ -450,12 +465,13 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!ok) {
                 // products under way read shared memory and write TMEM: wait for them before leaving
-                *abort_flag = 1;
+                if (lane == 0) lp_abort(H);
+                __syncwarp();
                 if (lp_elect())
                     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                                  ::"r"(smem_u32(&H.drain)) : "memory");
                 __syncwarp();
-                if (!lp_wait(smem_u32(&H.drain), 0, kBulkWaitTries)) *abort_flag = 2;
+                lp_wait(smem_u32(&H.drain), 0, kBulkWaitTries);
             }
         }
     } else {
@@ -556,7 +572,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
                 asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];"
                              ::"r"(lp_leader(smem_u32(&H.acc_empty[b]))) : "memory");
         }
-        if (!ok && lane == 0) *abort_flag = 1;
+        if (!ok && lane == 0) lp_abort(H);
     }
     __syncwarp();
     __syncthreads();
@@ -564,8 +580,27 @@ __global__ void __launch_bounds__(kLpThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     lp_cluster_sync();                                         // the peer's barriers and tiles are no longer used
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    // products that would not end keep their columns rather than have them freed underneath
-    if (warp == 1 && H.abort != 2)
+    if (*abort_flag) {
+        // Copies may still be under way to either CTA, which may not leave before them.  They are counted by the
+        // leader's barriers; where one CTA has loaded a stage and the other has not, the barrier is told so.  (Neither
+        // is ever more than a ring of stages ahead: a slot is free once the products have used both CTAs' tiles.)
+        if (leader && warp == 0) {
+            const uint32_t mine = H.issued, theirs = lp_of_peer(H.issued), last = max(mine, theirs);
+            if (lane == 0) {
+                for (uint32_t i = mine; i < theirs; i++)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                                 ::"r"(smem_u32(&H.full[i % kLpStages])), "r"(lp_of_peer(H.bytes[i % kLpStages])) : "memory");
+                for (uint32_t i = theirs; i < mine; i++)
+                    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;"
+                                 ::"r"(smem_u32(&H.full[i % kLpStages])), "r"(H.bytes[i % kLpStages]) : "memory");
+            }
+            __syncwarp();
+            for (uint32_t i = last - min(last, (uint32_t)kLpStages); i < last; i++)
+                lp_wait(smem_u32(&H.full[i % kLpStages]), (i / kLpStages) & 1u, kBulkWaitTries);
+        }
+        lp_cluster_sync();
+    }
+    if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
