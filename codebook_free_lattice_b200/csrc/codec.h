@@ -42,5 +42,5 @@ extern std::atomic<uint32_t> g_first_wait_tries, g_mma_wait_tries;
 // argument checks of a compressed weight (llvq.cu)
 llvq_status check_weight(const llvq_codec *c, const llvq_weight *w);
 // shared-memory limits of the linear layers' kernels and pairs, on the codec's device (linear.cu)
-void set_linear_attrs(llvq_codec *c);
+cudaError_t set_linear_attrs(llvq_codec *c);
 }  // namespace llvq

@@ -339,52 +339,54 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     return refuse(cudaGetErrorString(e), LLVQ_ERR_CUDA);
 }
 
-template <class K>
-void allow(K kernel, size_t smem) {
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
+// The largest dynamic shared memory of every kernel of the layers; the first error.
 template <bool GROUPED>
-void allow_all() {
+cudaError_t allow_all() {
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel, size_t smem) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    };
     allow(k_dequant48<kDqWeights, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqWeights, 1, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqTwoParts, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqTwoParts, 1, GROUPED>, kSmemLimit);
-    allow(k_dequant<Dec72, kDqTwoParts, GROUPED>, kSmemLimit);
-    allow(k_dequant<Dec96, kDqTwoParts, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDots, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDots, 1, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDotsFar, 0, GROUPED>, kSmemLimit);
     allow(k_dequant48<kDqDotsFar, 1, GROUPED>, kSmemLimit);
-    allow(k_dequant<Dec72, kDqDotsFar, GROUPED>, kSmemLimit);
-    allow(k_dequant<Dec96, kDqDotsFar, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec72, kDqWeights, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec72, kDqTwoParts, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec72, kDqDots, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec72, kDqDotsFar, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec96, kDqWeights, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec96, kDqTwoParts, GROUPED>, kSmemLimit);
     allow(k_dequant<Dec96, kDqDots, GROUPED>, kSmemLimit);
+    allow(k_dequant<Dec96, kDqDotsFar, GROUPED>, kSmemLimit);
     allow(k_linear_product<GROUPED, false, __half>, lp_smem(GROUPED));
     allow(k_linear_product<GROUPED, true, __half>, lp_smem(GROUPED));
     allow(k_linear_product<GROUPED, false, __nv_bfloat16>, lp_smem(GROUPED));
     allow(k_linear_product<GROUPED, true, __nv_bfloat16>, lp_smem(GROUPED));
+    return e;
 }
 
 }  // namespace
 
-void llvq::set_linear_attrs(llvq_codec *c) {
+cudaError_t llvq::set_linear_attrs(llvq_codec *c) {
     static_assert(dq48_fixed() + dq_tail(kDqWeights, true, 0, 0) <= kSmemLimit && lp_smem(true) <= kSmemLimit, "shared memory of an SM");
-    allow_all<false>();
-    allow_all<true>();
+    cudaError_t e = allow_all<false>();
+    if (e == cudaSuccess) e = allow_all<true>();
+    if (e != cudaSuccess) return e;
     // pairs of CTAs that are resident at once, one CTA per SM
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c->num_sms / 2 * 2));
     cfg.blockDim = dim3(kLpThreads);
     cfg.dynamicSmemBytes = lp_smem(true);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear_product<true, false, __half>, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        n = c->num_sms / 2;
-    }
+    e = cudaOccupancyMaxActiveClusters(&n, k_linear_product<true, false, __half>, &cfg);
+    if (e != cudaSuccess) return e;
     c->pairs = std::max(1, std::min(n, c->num_sms / 2));
     encode_tiled();                                        // looked up here, not inside a stream capture
+    return cudaSuccess;
 }
 
 extern "C" {

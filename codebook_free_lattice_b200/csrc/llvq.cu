@@ -976,6 +976,19 @@ void set_kernel_attrs() {
     });
 }
 
+// The last step of making a codec; one whose kernels cannot be set up is not handed out.
+llvq_status finish_codec(llvq_codec *c, llvq_codec **out) {
+    const cudaError_t e = set_linear_attrs(c);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        g_last_error = std::string("setting up the linear layers' kernels: ") + cudaGetErrorString(e);
+        llvq_codec_destroy(c);
+        return LLVQ_ERR_CUDA;
+    }
+    *out = c;
+    return LLVQ_OK;
+}
+
 llvq_status codec_create96(llvq_codec **out) {
     llvq_codec *c = new llvq_codec;
     c->index_bits = 96;
@@ -1003,9 +1016,7 @@ llvq_status codec_create96(llvq_codec **out) {
         return st;
     }
     set_kernel_attrs();
-    set_linear_attrs(c);
-    *out = c;
-    return LLVQ_OK;
+    return finish_codec(c, out);
 }
 
 }  // namespace
@@ -1163,9 +1174,7 @@ llvq_status llvq_codec_create(int32_t index_bits, llvq_codec **out) {
         return LLVQ_ERR_CUDA;
     }
     set_kernel_attrs();
-    set_linear_attrs(c);
-    *out = c;
-    return LLVQ_OK;
+    return finish_codec(c, out);
 }
 
 void llvq_codec_destroy(llvq_codec *c) {

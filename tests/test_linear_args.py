@@ -212,3 +212,16 @@ def test_workspace_of_a_gated_fp16_layer(L, bare, bits):
     assert need() == need(x_stride=1003) == need(experts=4) == 200 * 2048 * 2 + rest + 64 * 2048 * 2      # 42 blocks of 48
     assert need(dtype=1) == 200 * 1024 * 2 + rest + 64 * 1024 * 2 + 256
     assert need(tokens=2) == up256(2 * 200 * 42 * 4)
+
+
+def test_a_failed_setup_is_reported(L, tmp_path):
+    """Kernels whose limits cannot be set (here: there is no device) fail the codec's creation, not a later launch."""
+    if torch.cuda.is_available():
+        pytest.skip("a device is present")
+    from codebook_free_lattice_b200 import build
+    (tmp_path / "setup.cu").write_text('#include "codec.h"\nextern "C" int setup() { llvq_codec c; c.num_sms = 148; '
+                                       'return (int)llvq::set_linear_attrs(&c); }\n')
+    so = str(tmp_path / "setup.so")
+    subprocess.run([build.NVCC, "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "--expt-relaxed-constexpr", "-I", CSRC,
+                    "-Xcompiler", "-fPIC", "-shared", "-o", so, str(tmp_path / "setup.cu"), L.LIB_PATH], check=True, capture_output=True)
+    assert C.CDLL(so).setup() != 0
