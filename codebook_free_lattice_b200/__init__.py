@@ -9,6 +9,7 @@ fallback: importing the binding fails if libllvq.so is missing or cannot be load
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +80,8 @@ def lib() -> C.CDLL:
         L.llvq_codec_destroy.restype = None
         L.llvq_codec_info.argtypes = [C.c_void_p, C.POINTER(C.c_int32), C.POINTER(C.c_uint64),
                                       C.POINTER(C.c_uint64), C.POINTER(C.c_int64)]
+        L.llvq_codec_device.argtypes = [C.c_void_p]
+        L.llvq_codec_device.restype = C.c_int32
         L.llvq_decode.argtypes = [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_void_p]
         L.llvq_gemv.argtypes = [C.c_void_p, C.POINTER(llvq_weight), C.c_void_p, C.c_void_p, C.c_void_p]
         L.llvq_gemm_smallbatch.argtypes = [C.c_void_p, C.POINTER(llvq_weight), C.c_void_p, C.c_int32,
@@ -114,7 +117,7 @@ EXPORTED = ("llvq_codec_create", "llvq_codec_destroy", "llvq_codec_info", "llvq_
             "llvq_gemv", "llvq_gemm_smallbatch", "llvq_get_error", "llvq_status_string",
             "llvq_decode_noalloc", "llvq_class_table96", "llvq_last_error_message", "llvq_encode",
             "llvq_set_wait_polls", "llvq_search", "llvq_spherical_gptq", "llvq_spherical_gptq_workspace",
-            "llvq_linear", "llvq_linear_grouped", "llvq_linear_workspace")
+            "llvq_linear", "llvq_linear_grouped", "llvq_linear_workspace", "llvq_codec_device")
 
 
 def llvq_set_wait_polls(table_polls: int = 0xFFFFFFFF, mma_polls: int = 0xFFFFFFFF) -> None:
@@ -176,8 +179,13 @@ class Codec:
         self.n_points = (hi.value << 64) | lo.value
         self.n_classes = nc.value
         self.word_bytes = 8 if index_bits == 48 else 16
+        self._device_index = lib().llvq_codec_device(h)
+
+    @functools.cached_property
+    def device(self):
+        """The torch device that holds the tables."""
         import torch
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        return torch.device("cuda", self._device_index)
 
     @property
     def handle(self) -> C.c_void_p:

@@ -1208,6 +1208,8 @@ llvq_status llvq_codec_info(const llvq_codec *c, int32_t *max_shell, uint64_t *l
     return LLVQ_OK;
 }
 
+int32_t llvq_codec_device(const llvq_codec *c) { return c ? c->device : -1; }
+
 llvq_status llvq_decode(const llvq_codec *c, const void *d_words, int32_t word_bytes, int64_t n,
                         int8_t *d_out, void *stream) {
     if (!c || n < 0) return LLVQ_ERR_ARG;

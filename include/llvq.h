@@ -120,6 +120,9 @@ void llvq_codec_destroy(llvq_codec *codec);
  * pointer may be NULL. */
 llvq_status llvq_codec_info(const llvq_codec *codec, int32_t *max_shell, uint64_t *n_points_lo,
                             uint64_t *n_points_hi, int64_t *n_classes);
+/* The CUDA device that holds the codec's tables (the one that was current when it was created), which every
+ * call takes its tensors on; -1 for NULL.  The paper has no counterpart. */
+int32_t llvq_codec_device(const llvq_codec *codec);
 
 /* Decode n packed words (their index bits; gain bits are ignored) into int8 d_out [n][24]
  * (the lattice coordinates), by the hierarchical bijection of papernotes.org notes, 关键设计 2

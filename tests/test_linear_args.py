@@ -225,3 +225,25 @@ def test_a_failed_setup_is_reported(L, tmp_path):
     subprocess.run([build.NVCC, "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "--expt-relaxed-constexpr", "-I", CSRC,
                     "-Xcompiler", "-fPIC", "-shared", "-o", so, str(tmp_path / "setup.cu"), L.LIB_PATH], check=True, capture_output=True)
     assert C.CDLL(so).setup() != 0
+
+
+def test_a_codec_is_made_without_torch(L, monkeypatch):
+    """A codec needs no torch before its first call with tensors; it knows its device from the library."""
+    import sys
+    made = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: {"llvq_codec_device": 3}.get(name, made.append(name) or 0)
+
+    monkeypatch.setattr(L, "_lib", Library())
+    with monkeypatch.context() as m:
+        m.setitem(sys.modules, "torch", None)
+        codec = L.Codec(48)
+    assert codec.device == torch.device("cuda", 3) and "llvq_codec_create" in made
+    codec.close()
+    assert codec.device == torch.device("cuda", 3)
+
+
+def test_device_of_a_codec(L, bare):
+    assert L.lib().llvq_codec_device(bare[48]) == 0 and L.lib().llvq_codec_device(None) == -1
