@@ -261,6 +261,8 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     if (q->tokens == 0 || p.rows == 0) return LLVQ_OK;
     if (!q->x || !q->y) return refuse("null x or y");
     if (q->x == q->y) return refuse("y is x: other outputs still need what would be overwritten");
+    if (q->residual == q->y && q->tokens > 1 && q->residual_stride != q->y_stride)
+        return refuse("the residual is y with another stride: rows are overwritten that others still add");
     if (grouped != (q->offsets != nullptr)) return refuse(grouped ? "null offsets" : "offsets without groups");
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes) return refuse("workspace null, misaligned or too small");
     DeviceScope scope(c->device);

@@ -113,6 +113,15 @@ def test_null_and_workspace(L, bare):
     assert lib.llvq_linear_workspace(bare[48], C.byref(w), C.byref(q)) == 0
 
 
+@pytest.mark.parametrize("tokens,stride,refused", ((5, 0, True), (5, 65, True), (1, 0, False), (5, 64, False)))
+def test_a_residual_at_y_has_its_stride(L, bare, tokens, stride, refused):
+    """Rows of y may be the residual's, in place; one of them added to all, or rows between them, would change under the
+    call.  (A call that passes this check is stopped by its workspace.)"""
+    w, q = weight(L), call(L, tokens=tokens, residual=2 * ADDRESS, residual_stride=stride)
+    assert L.lib().llvq_linear(bare[48], C.byref(w), C.byref(q), None, 0, None) == L.LLVQ_ERR_ARG
+    assert (b"residual" in L.lib().llvq_last_error_message()) == refused
+
+
 def test_nothing_to_do_is_ok_without_pointers(L, bare):
     lib = L.lib()
     w, q = weight(L), call(L, tokens=0, x=None, y=None)
