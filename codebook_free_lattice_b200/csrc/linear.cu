@@ -46,8 +46,8 @@ struct Plan {
     int stage = 0;                                         // LinArgs::stage
     long long held = 0;                                    // rows of the decoded weight
     long long w_pitch = 0, xs_pitch = 0;
-    bool far = false;                                      // ... with the activations in the workspace
     bool dots = false;                                     // few tokens: no decoded weight
+    bool far = false;                                      // ... with the activations in the workspace
     int parts = 1, terms = 0;                              // LinArgs::parts, terms
     size_t w = 0, row_scale = 0, counters = 0, partial = 0, xs = 0, token_scale = 0, bytes = 0;
 };
@@ -115,8 +115,6 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
     // only experts that have a token are decoded, and there are at most as many as tokens
     p.held = (long long)p.rows * std::min<long long>(p.experts, std::max<long long>(q->tokens, 1));
     if ((p.held + c->num_sms - 1) / c->num_sms + 2 > kMaxRunRows) return refuse("too many rows", LLVQ_ERR_UNSUPPORTED);
-    const bool direct = aligned(q->x, 16) && (q->tokens <= 1 || q->x_stride % 8 == 0);
-    p.stage = q->dtype == LLVQ_DTYPE_BF16 ? 2 : direct ? 0 : 1;
     // whole 128-byte lines per row: a box row that straddles two lines costs the tensor copies twice
     p.w_pitch = ((long long)w->blocks_per_row * 24 + 63) / 64 * 64;
     p.xs_pitch = ((long long)w->cols + 63) / 64 * 64;
@@ -140,6 +138,8 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         p.bytes = at;
         return LLVQ_OK;
     }
+    // more than two tokens from here on
+    p.stage = q->dtype == LLVQ_DTYPE_BF16 ? 2 : aligned(q->x, 16) && q->x_stride % 8 == 0 ? 0 : 1;
     if (q->gated && q->dtype == LLVQ_DTYPE_FP16) {
         p.parts = 2;
         p.stage = 1;
@@ -322,9 +322,7 @@ llvq_status run_linear(const llvq_codec *c, const llvq_weight *w, const llvq_lin
     LpMaps m;
     bool ok = make_map(m.w, l.W, p.held, l.terms, l.ldw, 128);
     const void *x = p.stage ? (const void *)l.Xs : q->x;
-    // the pitch of a single row is never used, but has to be one that a map takes
-    const long long pitch = p.stage ? p.xs_pitch : q->tokens > 1 ? q->x_stride : p.xs_pitch;
-    for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.terms, pitch, 128 >> b);
+    for (int b = 0; b < 4; b++) ok = ok && make_map(m.x[b], x, q->tokens, l.terms, p.stage ? p.xs_pitch : q->x_stride, 128 >> b);
     if (!ok) return refuse("sizes or strides beyond a tensor map", LLVQ_ERR_UNSUPPORTED);
     cudaError_t e = cudaSuccess;
     LinArgs first = l;
