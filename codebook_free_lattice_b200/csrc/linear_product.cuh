@@ -192,7 +192,7 @@ __device__ __noinline__ LpUnit lp_unit(const LpArgs &a, const LpShared &H, int u
 // Measured on 74 pairs: a stage of 64 columns takes 0.33 us with 256 tokens and no less than 0.27 us; the
 // epilogue 0.6 us and 0.3 us per 32 tokens, under the next tile's products but for the last; parts of a split
 // tile 3 us and 0.4 us per 32 tokens more.  Whole tiles go in rounds of all pairs, the rest is split along K while pairs would idle.
-__device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int &split) {
+__host__ __device__ __forceinline__ int lp_cost(int tiles, int cap, int pairs, int nk, int &split) {
     const int stage = max(270, 330 * cap / kLinTokens), ends = 600 + 10 * cap;
     const int rest = tiles % pairs;
     long long ns = (long long)(tiles / pairs) * max(nk * stage, ends) + ends;
