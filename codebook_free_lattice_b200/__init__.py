@@ -331,15 +331,14 @@ class Codec:
                              1 if gated else 0, experts, x.data_ptr(), x_stride, bias_ptr, res_ptr, res_stride,
                              y.data_ptr(), y_stride, off_ptr)
         L, wp, qp = lib(), C.byref(w), C.byref(q)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+        raw = torch._C._cuda_getCurrentRawStream(on) if stream is None else stream.cuda_stream
         need = L.llvq_linear_workspace(self._h, wp, qp)
         if workspace is None or workspace.numel() < need:
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
                 workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
         elif workspace.get_device() != on or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
             raise TypeError(f"{name}: workspace is {workspace.dtype} on {workspace.device}, not contiguous uint8 on {self.device}")
-        _check(call(self._h, wp, qp, workspace.data_ptr(), workspace.numel(), stream.cuda_stream), name)
+        _check(call(self._h, wp, qp, workspace.data_ptr(), workspace.numel(), raw), name)
         return workspace
 
     def get_error(self, stream=None) -> int:

@@ -26,8 +26,3 @@ def test_only_constant_data_is_read_by_non_coherent_loads():
             found += 1
             assert any(re.match(p, argument) for p in constant), (os.path.basename(f), argument)
     assert found >= 8
-
-
-def test_the_binding_keeps_to_public_names():
-    text = open(os.path.join(os.path.dirname(CSRC), "__init__.py")).read()
-    assert "torch._" not in text
