@@ -164,6 +164,14 @@ def _stream(stream) -> C.c_void_p:
     return C.c_void_p(stream.cuda_stream)
 
 
+def _current_raw_stream(device) -> int:
+    """The handle of a device's current stream.  torch gives the handle by itself in 0.06 us, under a name that is not
+    public; a torch without it gives a Stream object, in 2.1 us."""
+    import torch
+    by_index = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if by_index is None else by_index(device.index)
+
+
 class Codec:
     """Decode and encode tables of one index budget (48, 72 or 96 bits) on the current CUDA device.
     close() (or leaving a `with` block) releases them at once; the 96-bit tables hold 23.6 GB."""
@@ -331,7 +339,7 @@ class Codec:
                              1 if gated else 0, experts, x.data_ptr(), x_stride, bias_ptr, res_ptr, res_stride,
                              y.data_ptr(), y_stride, off_ptr)
         L, wp, qp = lib(), C.byref(w), C.byref(q)
-        raw = torch._C._cuda_getCurrentRawStream(on) if stream is None else stream.cuda_stream
+        raw = _current_raw_stream(self.device) if stream is None else stream.cuda_stream
         need = L.llvq_linear_workspace(self._h, wp, qp)
         if workspace is None or workspace.numel() < need:
             with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):

@@ -256,3 +256,13 @@ def test_a_codec_is_made_without_torch(L, monkeypatch):
 
 def test_device_of_a_codec(L, bare):
     assert L.lib().llvq_codec_device(bare[48]) == 0 and L.lib().llvq_codec_device(None) == -1
+
+
+def test_current_stream_without_the_private_accessor(L, monkeypatch):
+    """The layers take the current stream's handle by a name of torch that is not public only where torch has it."""
+    device = torch.device("cuda", 2)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+    assert L._current_raw_stream(device) == 102
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: type("S", (), {"cuda_stream": 7 + d.index}))
+    assert L._current_raw_stream(device) == 9
