@@ -308,14 +308,25 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int u
 // Activations, four values at a time and out of line: the code of one activation is fetched once, and
 // a kernel that needs none of it does not step over it.  Each keeps the relative accuracy of its negative tail,
 // which a gate can bring back: z P(z) with P(z) = erfc(-z / sqrt 2) / 2 for gelu, and z e^u / (1 + e^u) below
-// zero for the others, so that the denominator lies between 1 and 2.  The quick division is good to a few fp32 steps,
+// zero for the others, so that the denominator lies between 1 and 2.  erfc(x) e^x^2 is t q(t) with t = 1 / (1 + 3/8 x) and
+// q of degree 6, the polynomial whose largest relative error on 0 <= x <= 9.5 (beyond, P leaves fp32's range) is
+// least, 6.3e-7, found as a linear program over 4000 Chebyshev points; 1.0e-6 as evaluated in fp32.  (With erfcf
+// 333 tokens over 1001 x 999 take 19.4 us instead of 18.6.)  The quick division is good to a few fp32 steps,
 // the quick exponential to 1.2 |u| more: 2^-16 where e^u is about to leave fp32's range, an eighth of a 16-bit
 // half step.
 enum LinAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 __device__ __forceinline__ float lin_activate1(float z, int act) {
     if (act == kActRelu) return z < 0.f ? 0.f : z;                              // NaN stays
     if (act == kActGelu) {
-        const float tail = 0.5f * erfcf(fabsf(z) * 0.70710678118654752f);       // P(-|z|)
+        const float x = fabsf(z) * 0.70710678118654752f;
+        const float t = __fdividef(1.f, fmaf(0.375f, x, 1.f));
+        float q = fmaf(-0.135078266f, t, 0.387873024f);
+        q = fmaf(q, t, -0.129502341f);
+        q = fmaf(q, t, 0.282991320f);
+        q = fmaf(q, t, 0.166691899f);
+        q = fmaf(q, t, 0.215683907f);
+        q = fmaf(q, t, 0.211339846f);
+        const float tail = 0.5f * q * t * __expf(-x * x);                       // P(-|z|)
         return z * (z < 0.f ? tail : 1.f - tail);
     }
     const float u = act == kActSilu ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);     // 2 sqrt(2 / pi)

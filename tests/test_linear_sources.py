@@ -26,3 +26,18 @@ def test_only_constant_data_is_read_by_non_coherent_loads():
             found += 1
             assert any(re.match(p, argument) for p in constant), (os.path.basename(f), argument)
     assert found >= 8
+
+
+def test_the_erfc_of_gelu():
+    """The coefficients in the source against scipy's scaled complementary error function, in relative terms: 1e-6 from
+    zero to where erfc leaves fp32's range."""
+    import numpy as np
+    special = __import__("pytest").importorskip("scipy.special")
+    text = open(os.path.join(CSRC, "linear_common.cuh")).read()
+    body = text[text.index("const float t = __fdividef(1.f, fmaf("):text.index("const float tail")]
+    p, *_ = re.findall(r"fmaf\(([0-9.]+)f, x", body)
+    q = [float(v) for v in re.findall(r"(-?\d\.\d+)f, t,", body)] + [float(v) for v in re.findall(r", t, (-?\d\.\d+)f\)", body)]
+    assert len(q) == 7
+    x = np.linspace(0, 10, 100001)
+    t = 1 / (1 + float(p) * x)
+    assert np.abs(np.polyval(q, t) * t / special.erfcx(x) - 1).max() < 1e-6
