@@ -13,7 +13,7 @@ using namespace llvq;
 namespace {
 
 constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
-// Activations of this many values, or in rows this long, are restated by a kernel of their own, others beside the
+// Activations of this many values, or in rows this long, that are restated at all are restated by a kernel of their own, others beside the
 // decode, where a warp takes a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096 over 4096 x 4096 133
 // against 137, 512 over 1024 x 1024 26 against 19 (one more launch).
 constexpr long long kStageValues = 1 << 21;
@@ -69,7 +69,9 @@ int dequant_ctas(int bits) { return bits == 48 ? 1 : bits == 72 ? Dec72::kCtasPe
 // written bytes per block once.  Measured on one matrix, with and without a decoded weight: 4096 x 4096, 1 / 2 / 3
 // tokens 27.8 / 30.5 / 33.5 us against 37.4; 22016 x 4096, 1 / 3 tokens 103 / 130 us against 145.  Over experts
 // what counts is how many tokens one gets, two on average: 8 tokens over 4 experts of 2816 x 2048 40.6 us against
-// 41.9, 16 over 8 of 1408 x 1024 27.0 against 27.6.
+// 41.9, 16 over 8 of 1408 x 1024 27.0 against 27.6.  Larger budgets decode more slowly, in both forms, and turn at
+// the same place: 4096 x 4096, 1 / 3 / 4 fp16 tokens at 72 bits 72.2 / 76.8 / 78.6 us against 79.5 (bf16: 4 tokens 80.9
+// against 79.7), at 96 bits 141.6 / 146.8 / 149.3 against 152.5; 16 over 8 experts 64.0 against 67.3 and 121 against 132.
 //
 // Activations that do not fit in shared memory beside the decoder's tables are restated in the workspace and read
 // through L1, dearer per token: two tokens of one matrix (4096 x 11008: 70.7 us against 74.5; one of 8192 x 28672

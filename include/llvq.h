@@ -265,9 +265,11 @@ llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int3
  * `dtype`; sums, bias, activation and residual are held in fp32 and y is rounded once.  A few tokens (up to
  * 3, or 16 over experts) are multiplied block by block with the exact integers, gains in fp32; for more the
  * weight is decoded into the workspace, each weight rounded to 11 significant bits (fp16 with a power of
- * two per row), for bf16 activations too; a gated fp16 layer, which multiplies two sums, keeps 22 bits in two
- * fp16 values, at twice the products.  Rows of x, residual and y may have any stride and start at any
- * 2-byte aligned address; rows of y may be the residual's (same address and stride), but not x's.
+ * two per row; fewer below 2^-24 of the row's largest gain), for bf16 activations too; a gated fp16 layer, which
+ * multiplies two sums, keeps 22 bits in two fp16 values, at twice the products.  Against exact sums the output is then
+ * 1.01 (bf16), 1.3 (fp16) and 1.00 times (gated fp16) as far off as its own rounding.  Rows of x, residual and y may
+ * have any stride from their length up and start at any 2-byte aligned address; rows of y may be the residual's (same
+ * address and stride), but not x's.
  *
  * llvq_linear: `experts` 0 or 1, `offsets` NULL: tokens rows of x, one matrix.
  * llvq_linear_grouped: `experts` (1 .. 2048) matrices of rows / experts rows each, stacked in w; bias
@@ -294,10 +296,10 @@ typedef struct {
 
 /* Bytes of workspace that a call needs (0 when its sizes or types are refused): the decoded weight of the
  * experts that can have tokens (48 bytes per block, 96 for gated fp16), partial sums (19.4 MB on 148 SMs), and for
- * bf16 or unaligned x the activations restated in fp16 (for gated fp16 twice over); for a few tokens, 4 bytes per block and token.  Depends on
- * x's address only by its 16-byte alignment; the sizes and x must be set in `call`, its other pointers need
- * not be.  A call with experts >= 1 is
- * taken as grouped. */
+ * bf16 or unaligned x the activations restated in fp16 (for gated fp16 twice over); for a few tokens, 4 bytes per
+ * token and block of the experts that can have one, min(experts, tokens) of them (a token uses those of its own
+ * expert only).  Depends on x's address only by its 16-byte alignment; the sizes and x must be set in `call`, its
+ * other pointers need not be.  A call with experts >= 1 is taken as grouped. */
 size_t llvq_linear_workspace(const llvq_codec *codec, const llvq_weight *w, const llvq_linear_call *call);
 
 /* The layer: two launches on `stream` (decode, then product with epilogue), three where many activations are
