@@ -13,9 +13,9 @@ using namespace llvq;
 namespace {
 
 constexpr int kMaxColumnBlocks = 0xFFFF;                   // column field of a record
-// Activations of this many values, or in rows this long, that are restated at all are restated by a kernel of their own, others beside the
-// decode, where a warp takes a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096 over 4096 x 4096 133
-// against 137, 512 over 1024 x 1024 26 against 19 (one more launch).
+// Activations of this many values, or in rows this long, that are restated at all are restated by a kernel of their
+// own, others beside the decode, where a warp takes a token: 8192 tokens over 2048 x 5504 168 us against 203, 4096
+// over 4096 x 4096 133 against 137, 512 over 1024 x 1024 26 against 19 (one more launch).
 constexpr long long kStageValues = 1 << 21;
 constexpr int kStageCols = 4096;
 // A wait of the product covers a whole tile (milliseconds for the longest rows), not one round of few products:

@@ -20,7 +20,7 @@
 // the epilogue, exactly.  A bf16 weight would have lost 3 bits that fp16 keeps.
 //
 // Against the definition in 64 bits, one fp16 value per weight leaves a bf16 output 1.01 times as far off as its
-// own rounding does, and a plain fp16 output 1.3 times (the weight's rounding is as large as the output's, and
+// own rounding does, and a plain fp16 output 1.3 to 1.45 times (the weight's rounding is as large as the output's, and
 // independent of it).  A gated fp16 output multiplies two such sums and would be 1.75 times as far off (3.6e-4
 // against 2.1e-4), so its weights have two fp16 values, the second the rest of the first: 22 bits, 1.00 times,
 // for twice the products and twice the decoded weight.  A block's 24 values and their 24 rests follow one another,
@@ -311,9 +311,8 @@ __global__ void __launch_bounds__(kLinStageMost) k_linear_stage(LinArgs a, int u
 // zero for the others, so that the denominator lies between 1 and 2.  erfc(x) e^x^2 is t q(t) with t = 1 / (1 + 3/8 x) and
 // q of degree 6, the polynomial whose largest relative error on 0 <= x <= 9.5 (beyond, P leaves fp32's range) is
 // least, 6.3e-7, found as a linear program over 4000 Chebyshev points; 1.0e-6 as evaluated in fp32.  (With erfcf
-// 333 tokens over 1001 x 999 take 19.4 us instead of 18.6.)  The quick division is good to a few fp32 steps,
-// the quick exponential to 1.2 |u| more: 2^-16 where e^u is about to leave fp32's range, an eighth of a 16-bit
-// half step.
+// 333 tokens over 1001 x 999 take 19.4 us instead of 18.6.)  The quick division is good to a few fp32 steps, the quick
+// exponential to 1.2 |u| more: 2^-16 where e^u is about to leave fp32's range, a thirty-second of fp16's half step.
 enum LinAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 __device__ __forceinline__ float lin_activate1(float z, int act) {
     if (act == kActRelu) return z < 0.f ? 0.f : z;                              // NaN stays

@@ -1,13 +1,15 @@
 // linear_dequant.cuh -- the first kernel of a compressed linear layer: every block of the experts
 // that have tokens is decoded once, and written as 24 scaled fp16 weights (linear_common.cuh; a gated fp16
-// layer's in two parts) or, for a few tokens, multiplied with them at once (k_linear_finish then adds each row's dot products in order).
+// layer's in two parts) or, for a few tokens, multiplied with them at once (k_linear_finish then adds each row's dot
+// products in order).
 //
 // "Leech Lattice Vector Quantization for Efficient LLM Compression", papernotes.org notes,
 // 方法详解 / 关键设计 2: index -> shell, class, codeword, signs, arrangement -> integer vector.
 //
-// Integer work bounds it: about 700 thread instructions per 48-bit block, against 8 bytes read and 48
-// written.  Each CTA takes an equal run of blocks (not of rows: a run may begin and end inside a row, so
-// few long rows still spread over all SMs).  48-bit blocks use the warp-private rings of the fused GEMV
+// Integer work bounds it: about 700 thread instructions per 48-bit block, against 8 bytes read and 48 written (or 96,
+// in three stores of 32 bytes: 18944 x 8192 in 211 us against 188 for 48 bytes in three of 16; six of 16 took 344).
+// Each CTA takes an equal run of blocks (not of rows: a run may begin and end inside a row, so few long rows still
+// spread over all SMs).  48-bit blocks use the warp-private rings of the fused GEMV
 // (kernels_gemv48.cuh): a warp classifies 32 consecutive blocks, sorts them by coset into two rings and
 // decodes a ring once it holds 32, so that all lanes run the same decode.
 #pragma once

@@ -267,7 +267,7 @@ llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int3
  * weight is decoded into the workspace, each weight rounded to 11 significant bits (fp16 with a power of
  * two per row; fewer below 2^-24 of the row's largest gain), for bf16 activations too; a gated fp16 layer, which
  * multiplies two sums, keeps 22 bits in two fp16 values, at twice the products.  Against exact sums the output is then
- * 1.01 (bf16), 1.3 (fp16) and 1.00 times (gated fp16) as far off as its own rounding.  Rows of x, residual and y may
+ * 1.01 (bf16), 1.3 to 1.45 (fp16) and 1.00 times (gated fp16) as far off as its own rounding.  Rows of x, residual and y may
  * have any stride from their length up and start at any 2-byte aligned address; rows of y may be the residual's (same
  * address and stride), but not x's.
  *

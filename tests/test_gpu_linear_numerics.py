@@ -133,3 +133,20 @@ def test_tails_of_the_activations(codecs, act, low, gated, tokens, dtype):
     err = (y.double() - want).abs()
     bound = (u + 2.0 ** -14) * want.abs() + torch.finfo(dtype).tiny * u
     assert bool((err <= bound).all()), f"worst error {float((err / bound).max()):.3g} of its bound at z = {float(z[(err / bound).amax(0).argmax()])}"
+
+
+def test_uncoded_indices_in_a_gated_fp16_layer(codecs):
+    """They contribute nothing to either part of a weight, whatever the workspace held."""
+    import codebook_free_lattice_b200 as L
+    layer = Layer(codecs, 48, 40, 100, seed=5, bad=20)
+    layer.gains_d.view(torch.float16)[7] = 0
+    layer.dense[7] = 0
+    x = tokens_of(1, 30, 100, torch.float16)
+    y = torch.empty(30, 20, dtype=torch.float16, device="cuda")
+    layer.codec.get_error()
+    ws = layer.codec.linear(layer.weight, x, y, gated=True)
+    ws.fill_(0xFF)
+    layer.codec.linear(layer.weight, x, y, gated=True, workspace=ws)
+    want = definition(layer, x, "none")
+    assert rms(y - want) <= MARGIN * rms(want.half() - want) and bool((y[:, 7] == 0).all())
+    assert layer.codec.get_error() == L.LLVQ_FLAG_INDEX_RANGE
