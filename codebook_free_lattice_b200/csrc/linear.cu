@@ -72,14 +72,18 @@ int dequant_ctas(int bits) { return bits == 48 ? 1 : bits == 72 ? Dec72::kCtasPe
 // 41.9, 16 over 8 of 1408 x 1024 27.0 against 27.6.  Larger budgets decode more slowly, in both forms, and turn at
 // the same place: 4096 x 4096, 1 / 3 / 4 fp16 tokens at 72 bits 72.2 / 76.8 / 78.6 us against 79.5 (bf16: 4 tokens 80.9
 // against 79.7), at 96 bits 141.6 / 146.8 / 149.3 against 152.5; 16 over 8 experts 64.0 against 67.3 and 121 against 132.
+// Decoded weights of two parts (gated fp16) cost twice as much, and their layers turn later: 4096 x 4096, 4 / 5 tokens
+// 35.7 / 38.2 us against 43.5; 22016 x 2048, 4 / 6 / 8 tokens 78 / 93 / 109 against 107; 2048 x 2048, 6 / 8 tokens
+// 20.1 / 21.6 against 25; at 72 bits 22016 x 4096, 6 / 8 tokens 410 / 445 against 419; 9 over 3 experts of 5632 x 2048
+// 64 against 94, 16 over 8 of 1408 x 1024 29.4 against 39.9.
 //
 // Activations that do not fit in shared memory beside the decoder's tables are restated in the workspace and read
 // through L1, dearer per token: two tokens of one matrix (4096 x 11008: 70.7 us against 74.5; one of 8192 x 28672
 // 287 against 341), four over as many experts (1408 x 7168: 51 against 59), else one for every fourth expert (16 over
 // 64 of 1408 x 7168 196 against 221, over 16 162 against 121).
 enum Few { kManyTokens, kFewNear, kFewFar };
-Few few_tokens(int bits, bool grouped, int64_t tokens, int experts, int nb) {
-    const int near = std::max(3, experts > 1 ? std::min(2 * experts, kLinDots) : 1);
+Few few_tokens(int bits, bool grouped, bool two_parts, int64_t tokens, int experts, int nb) {
+    const int near = std::max(two_parts ? 6 : 3, experts > 1 ? std::min((two_parts ? 3 : 2) * experts, kLinDots) : 1);
     if (tokens > near) return kManyTokens;
     if (dequant_smem(bits, kDqDots, grouped, tokens, nb) <= kSmemLimit / dequant_ctas(bits) - 1024) return kFewNear;
     return tokens <= std::max({2, std::min(experts, 4), experts / 4}) ? kFewFar : kManyTokens;
@@ -127,7 +131,8 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
         at += round256(bytes);
         return here;
     };
-    const Few few = few_tokens(c->index_bits, grouped, q->tokens, p.experts, w->blocks_per_row);
+    const bool two_parts = q->gated && q->dtype == LLVQ_DTYPE_FP16;
+    const Few few = few_tokens(c->index_bits, grouped, two_parts, q->tokens, p.experts, w->blocks_per_row);
     if (few != kManyTokens) {
         p.dots = true;
         p.w = place((size_t)q->tokens * p.held * w->blocks_per_row * sizeof(float));
@@ -142,7 +147,7 @@ llvq_status make_plan(const llvq_codec *c, const llvq_weight *w, const llvq_line
     }
     // more than two tokens from here on
     p.stage = q->dtype == LLVQ_DTYPE_BF16 ? 2 : aligned(q->x, 16) && q->x_stride % 8 == 0 ? 0 : 1;
-    if (q->gated && q->dtype == LLVQ_DTYPE_FP16) {
+    if (two_parts) {
         p.parts = 2;
         p.stage = 1;
         p.terms = w->blocks_per_row * 48;

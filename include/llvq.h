@@ -263,8 +263,8 @@ llvq_status llvq_spherical_gptq(const llvq_codec *codec, int32_t max_shell, int3
  *   y[t][o] = act(z[t][o]) * z[t][F + o]          + residual[t][o]     gated = 1, o < F = rows / 2
  * (a gated weight holds the gate's rows, then the up projection's).  x, bias, residual and y are of
  * `dtype`; sums, bias, activation and residual are held in fp32 and y is rounded once.  A few tokens (up to
- * 3, or 16 over experts) are multiplied block by block with the exact integers, gains in fp32; for more the
- * weight is decoded into the workspace, each weight rounded to 11 significant bits (fp16 with a power of
+ * 3, of gated fp16 layers 6, or 16 over experts) are multiplied block by block with the exact integers, gains in
+ * fp32; for more the weight is decoded into the workspace, each weight rounded to 11 significant bits (fp16 with a power of
  * two per row; fewer below 2^-24 of the row's largest gain), for bf16 activations too; a gated fp16 layer, which
  * multiplies two sums, keeps 22 bits in two fp16 values, at twice the products.  Against exact sums the output is then
  * 1.01 (bf16), 1.3 to 1.45 (fp16) and 1.00 times (gated fp16) as far off as its own rounding.  Rows of x, residual and y may

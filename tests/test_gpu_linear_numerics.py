@@ -28,7 +28,7 @@ MARGIN = 1.05
 
 
 @pytest.mark.parametrize("bits,tokens,rows,cols,act,gain", [
-    (48, 5, 600, 700, "silu", "table"), (48, 40, 300, 1000, "silu", "direct"), (48, 300, 520, 480, "gelu_tanh", "table"),
+    (48, 6, 600, 700, "silu", "table"), (48, 7, 600, 700, "silu", "table"), (48, 40, 300, 1000, "silu", "direct"), (48, 300, 520, 480, "gelu_tanh", "table"),
     (72, 50, 130, 300, "none", "table")])
 def test_gated_fp16_is_as_good_as_its_rounding(codecs, bits, tokens, rows, cols, act, gain):
     layer = Layer(codecs, bits, rows, cols, gain, seed=tokens)

@@ -221,6 +221,10 @@ def test_workspace_of_a_gated_fp16_layer(L, bare, bits):
     assert need() == need(x_stride=1003) == need(experts=4) == 200 * 2048 * 2 + rest + 64 * 2048 * 2      # 42 blocks of 48
     assert need(dtype=1) == 200 * 1024 * 2 + rest + 64 * 1024 * 2 + 256
     assert need(tokens=2) == up256(2 * 200 * 42 * 4)
+    assert need(tokens=6) == up256(6 * 200 * 42 * 4) and need(tokens=7) > 200 * 2048 * 2
+    assert need(tokens=6, dtype=1) > 200 * 1024 * 2
+    assert need(tokens=6, experts=2) == up256(6 * 200 * 42 * 4) and need(tokens=15, experts=5) == up256(15 * 200 * 42 * 4)
+    assert need(tokens=16, experts=5) > 200 * 2048 * 2
 
 
 def test_a_failed_setup_is_reported(L, tmp_path):
